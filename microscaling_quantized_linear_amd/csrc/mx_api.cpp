@@ -11,10 +11,72 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "../../include/mx.h"
-#include "mx_kernels.h"
+#include "mx_host.h"
 
 namespace {
+
+// one entry per device ordinal: 0 not yet known (the zero-initialized
+// state, valid before any constructor runs), 1 not gfx950, 2 gfx950
+std::atomic<int> g_arch[64];
+
+// Dispatch trace: with MX_LOG=1 in the environment (read once per process)
+// every launch decision of the hot path goes to stderr as one line: entry
+// point, kernel and its launch plan, and the shape.  Off by default; no
+// output and no cost beyond one branch otherwise.
+bool log_on() {
+    static const bool on = [] {
+        const char *s = std::getenv("MX_LOG");
+        return s && s[0] && s[0] != '0';
+    }();
+    return on;
+}
+}  // namespace
+
+namespace mx {
+
+mx_status shape_ok(int elem, int layout, int64_t E, int64_t N, int64_t K) {
+    if (elem != E4M3 && elem != E2M1) return MX_ERR_UNSUPPORTED;
+    if (layout != ROW32 && layout != BLK32) return MX_ERR_UNSUPPORTED;
+    if (E < 1 || N < 16 || K < 32 || K % 32 != 0 || N % 16 != 0) return MX_ERR_SHAPE;
+    if (layout == BLK32 && N % 32 != 0) return MX_ERR_SHAPE;
+    return MX_OK;
+}
+
+mx_status device_ok() {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MX_ERR_DEVICE;
+    if (dev < 64) {
+        const int v = g_arch[dev].load();
+        if (v != 0) return v == 2 ? MX_OK : MX_ERR_DEVICE;
+    }
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MX_ERR_DEVICE;
+    const int ok = mx_arch_supported(prop.gcnArchName);
+    if (dev < 64) g_arch[dev].store(ok ? 2 : 1);
+    return ok ? MX_OK : MX_ERR_DEVICE;
+}
+
+void log_dispatch(const char *fmt, ...) {
+    if (!log_on()) return;
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    std::fprintf(stderr, "mx: %s\n", buf);
+}
+
+}  // namespace mx
+
+namespace {
+
+using mx::aligned16;
+using mx::device_ok;
+using mx::kMaxRsrc;
+using mx::launched;
+using mx::log_dispatch;
+using mx::round256;
+using mx::shape_ok;
 
 using mx::ACT_BF16;
 using mx::ACT_MXFP8;
@@ -23,8 +85,6 @@ using mx::BLK32;
 using mx::E2M1;
 using mx::E4M3;
 using mx::ROW32;
-
-constexpr int64_t kMaxRsrc = (int64_t(1) << 31) - 1;   // 32-bit buffer offsets
 
 // largest M served by the decode GEMV for W8A8; above it the GEMM runs
 constexpr int64_t kGemvMaxM = 64;
@@ -49,9 +109,6 @@ bool batch_invariant() {
 bool use_gemm(int act, int64_t M) {
     return act != ACT_BF16 && M > kGemvMaxM && !batch_invariant();
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // the W8A8 GEMV's launch plan (fails for more than 64 steps of K per wavefront)
 int env_int(const char *name) {
@@ -79,54 +136,6 @@ bool fused_quant_ok(int elem, int64_t N, int64_t K, int64_t M) {
            mx::gemv_w8_even(N, K, gemv_w8_plan(N, K, M));
 }
 
-mx_status shape_ok(int elem, int layout, int64_t E, int64_t N, int64_t K) {
-    if (elem != E4M3 && elem != E2M1) return MX_ERR_UNSUPPORTED;
-    if (layout != ROW32 && layout != BLK32) return MX_ERR_UNSUPPORTED;
-    if (E < 1 || N < 16 || K < 32 || K % 32 != 0 || N % 16 != 0) return MX_ERR_SHAPE;
-    if (layout == BLK32 && N % 32 != 0) return MX_ERR_SHAPE;
-    return MX_OK;
-}
-
-// one entry per device ordinal: 0 not yet known (the zero-initialized
-// state, valid before any constructor runs), 1 not gfx950, 2 gfx950
-std::atomic<int> g_arch[64];
-
-mx_status device_ok() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MX_ERR_DEVICE;
-    if (dev < 64) {
-        const int v = g_arch[dev].load();
-        if (v != 0) return v == 2 ? MX_OK : MX_ERR_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MX_ERR_DEVICE;
-    const int ok = mx_arch_supported(prop.gcnArchName);
-    if (dev < 64) g_arch[dev].store(ok ? 2 : 1);
-    return ok ? MX_OK : MX_ERR_DEVICE;
-}
-
-mx_status launched(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_LAUNCH; }
-
-// Dispatch trace: with MX_LOG=1 in the environment (read once per process)
-// every launch decision of the hot path goes to stderr as one line: entry
-// point, kernel and its launch plan, and the shape.  Off by default; no
-// output and no cost beyond one branch otherwise.
-bool log_on() {
-    static const bool on = [] {
-        const char *s = std::getenv("MX_LOG");
-        return s && s[0] && s[0] != '0';
-    }();
-    return on;
-}
-__attribute__((format(printf, 1, 2))) void log_dispatch(const char *fmt, ...) {
-    if (!log_on()) return;
-    char buf[256];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    std::fprintf(stderr, "mx: %s\n", buf);
-}
 const char *layout_name(int layout) { return layout == ROW32 ? "ROW32" : "BLK32"; }
 const char *elem_name(int elem) { return elem == E4M3 ? "E4M3" : "E2M1"; }
 
