@@ -377,6 +377,160 @@ mx_status mx_moe_down(int elem, int64_t E, int64_t H, int64_t inter,
                       const int32_t *topk_ids, const float *topk_weights,
                       void *y, void *ws, size_t ws_bytes, mx_stream_t stream);
 
+/* ---- Around the linear: the norm before it ---- */
+
+/* Residual addition, root-mean-square norm and the quantization of its output
+ * in one pass:
+ *   s[m][k] = bf16(x[m][k] + residual[m][k])      (residual NULL: s = x)
+ *   y[m][k] = bf16(s[m][k] * rsqrt(mean_k(s[m][k]^2) + eps) * weight[k])
+ * with the sum of squares and the products in fp32 (each bf16() one rounding to
+ * nearest even), and y handed out in the forms that mx_linear and
+ * mx_grouped_linear take:
+ *   act MX_ACT_BF16       y only
+ *   act MX_ACT_MXFP8      xq [M, ldq] and xcodes [M, ldc], as mx_quant_act of y
+ *   act MX_ACT_MXFP8_T16  xq and xcodes of mx_act_t16_sizes' sizes, every byte
+ *                         written, as mx_quant_act_t16 of y
+ * The bytes and codes are exactly those calls' on the bf16 y.  A row's outputs do not
+ * depend on M.
+ *   x        (device) bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K
+ *   residual (device, nullable) bf16 [M, ldr], the same rules
+ *   weight   (device) bf16 [K], 16-byte aligned
+ *   eps      >= 0
+ *   sum      (device, nullable) bf16 [M, lds]: receives s; may be x or residual
+ *            itself (the same pointer and leading dimension)
+ *   y        (device; nullable unless act is MX_ACT_BF16) bf16 [M, ldy]; may be x
+ *            or residual itself when sum is not
+ *   xq, xcodes (device; unused when act is MX_ACT_BF16): ldq % 16 == 0,
+ *            ldq >= K, ldc >= K / 32 (ldq, ldc unused for T16); 16-byte aligned
+ *            (xcodes of MX_ACT_MXFP8: any)
+ *   rule     as mx_quant_act (checked for every act)
+ * Rules: 1 <= M <= 4000000, 32 <= K <= 65536, K % 32 == 0.
+ * Errors: MX_ERR_UNSUPPORTED also when an output overlaps another buffer in
+ *   any other way than named above. */
+mx_status mx_add_rms_norm(int64_t M, int64_t K, const void *x, int64_t ldx, const void *residual,
+                          int64_t ldr, const void *weight, float eps, int act, int rule, void *sum,
+                          int64_t lds, void *y, int64_t ldy, void *xq, int64_t ldq, void *xcodes,
+                          int64_t ldc, mx_stream_t stream);
+
+/* ---- Experts over ragged row ranges (prompts, any number of tokens) ----
+ * mx_moe_linear serves decode steps (T * topk <= 4096, bf16 activations).
+ * These calls serve any number of tokens on the scaled matrix cores:
+ *   mx_moe_sort        the routed pairs in expert order
+ *   mx_grouped_linear  one product per expert on its rows, e.g. gate and up
+ *                      (MX_EPI_SILU), then down
+ *   mx_moe_combine     a token's expert outputs summed with their weights
+ * A pair is (token t, choice k), number t * topk + k. */
+
+/* Workspace bytes mx_moe_sort needs (0 for T * topk <= 2048). */
+mx_status mx_moe_sort_workspace(int64_t E, int64_t T, int64_t topk, size_t *bytes);
+
+/* The routed pairs in expert order, within an expert by pair number.
+ *   topk_ids (device) int32 [T, topk]; an id outside [0, E) takes no expert;
+ *            the same id twice in a token is two pairs
+ *   offsets  (device) int32 [E + 1]: expert e's pairs have places
+ *            offsets[e] .. offsets[e + 1] - 1; offsets[0] = 0
+ *   rows     (device) int32 [T topk]: the token of each place, -1 from
+ *            offsets[E] on
+ *   pos      (device) int32 [T, topk]: the place of each pair, -1 without an
+ *            expert
+ *   ws       (device) at least mx_moe_sort_workspace's bytes, 16-byte aligned
+ *            (may be NULL when that is 0)
+ * The result is the same in every run.
+ * Rules: 1 <= E <= 1024, T >= 1, 1 <= topk <= E, T * topk <= 4000000; the
+ * buffers must not overlap (MX_ERR_UNSUPPORTED). */
+mx_status mx_moe_sort(int64_t E, int64_t T, int64_t topk, const int32_t *topk_ids,
+                      int32_t *offsets, int32_t *rows, int32_t *pos, void *ws, size_t ws_bytes,
+                      mx_stream_t stream);
+
+/* Epilogues of mx_grouped_linear. */
+typedef enum { MX_EPI_NONE = 0, MX_EPI_SILU = 1 } mx_epi;
+
+/* Workspace bytes mx_grouped_linear needs: the rows' T16 activation
+ * (mx_act_t16_sizes of M rows, the first size rounded up to 256) when act is
+ * MX_ACT_MXFP8, whether prequantized or not; 0 when act is MX_ACT_MXFP8_T16. */
+mx_status mx_grouped_workspace(int elem, int layout, int64_t E, int64_t N, int64_t K, int64_t M,
+                               int act, int prequantized, size_t *bytes);
+
+/* Products grouped by expert:
+ *   z[i][n] = sum_k a[i][k] Wf[e][n][k]   for offsets[e] <= i < offsets[e + 1]
+ *   MX_EPI_NONE  y[i][n] = bf16(z[i][n]),                          N columns
+ *   MX_EPI_SILU  y[i][n] = bf16(silu(z[i][2 n]) * z[i][2 n + 1]),  N / 2 columns
+ *                (gate and up rows interleaved, as mx_moe_copies lays them out)
+ * fp32 accumulation, silu in fp32, one rounding.  Rows of y from offsets[E] on
+ * (and before offsets[0]) are left as they were.
+ *   w_packed, codes_packed (device) from mx_pack_weights(elem, layout, E, N, K)
+ *   M        rows of y, at least offsets[E]
+ *   offsets  (device) int32 [E + 1], not descending, within 0 .. M (mx_moe_sort's);
+ *            what lies outside is cut off
+ *   act MX_ACT_MXFP8: row i's activation is source row rows[i] (rows NULL: i,
+ *       then xrows >= M); a source row outside [0, xrows) counts as zeros.
+ *     x      (device) bf16 [xrows, ldx], 16-byte aligned, ldx % 8 == 0:
+ *            quantized with `rule` in the call; or, when xq and xcodes are both
+ *            non-NULL, x is unused and
+ *     xq     (device) e4m3 [xrows, ldq], 16-byte aligned, ldq % 16 == 0
+ *     xcodes (device) E8M0 [xrows, ldc]
+ *     rows   (device, nullable) int32 [M]
+ *     ws     (device) mx_grouped_workspace's bytes, 16-byte aligned
+ *   act MX_ACT_MXFP8_T16: xq, xcodes (device) hold the M rows in the T16 layout
+ *       (x, xrows, ldx, ldq, ldc, rule and ws unused, rows must be NULL)
+ *   y        (device) bf16 [M, ldy], 16-byte aligned, ldy % 8 == 0
+ * Built: E4M3 x {ROW32, BLK32} and E2M1 x ROW32; others, and MX_ACT_BF16, are
+ * MX_ERR_UNSUPPORTED, as are outputs that overlap an input.
+ * Rules: E <= 65535, 1 <= M <= 4000000; one expert's weights (K rounded up to
+ * 128) and 256 rows of y stay below 2 GiB, the staged activation below 256 GiB
+ * (MX_ERR_SHAPE).
+ * Asynchronous, allocates nothing, may be captured in a graph; calls that share
+ * a workspace must be ordered. */
+mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t K,
+                            const void *w_packed, const void *codes_packed, int64_t M,
+                            const int32_t *offsets, int act, int rule, int64_t xrows,
+                            const void *x, int64_t ldx, const void *xq, int64_t ldq,
+                            const void *xcodes, int64_t ldc, const int32_t *rows, int epi, void *y,
+                            int64_t ldy, void *ws, size_t ws_bytes, mx_stream_t stream);
+
+/* y[t][:] = sum_k topk_weights[t][k] ys[pos[t][k]][:], in k order in fp32, one
+ * rounding to bf16.  A place outside [0, M) adds nothing and its weight is not
+ * read; a token without places gets zeros.
+ *   ys  (device) bf16 [M, ldys], 16-byte aligned, ldys % 8 == 0, ldys >= N
+ *   pos (device) int32 [T, topk] (mx_moe_sort's)
+ *   topk_weights (device) fp32 [T, topk]
+ *   y   (device) bf16 [T, ldy], 16-byte aligned, ldy % 8 == 0, ldy >= N
+ * Rules: T, topk, M >= 1, T * topk and M <= 4000000, N % 8 == 0; y overlaps no
+ * input (MX_ERR_UNSUPPORTED). */
+mx_status mx_moe_combine(int64_t T, int64_t topk, int64_t N, int64_t M, const void *ys,
+                         int64_t ldys, const int32_t *pos, const float *topk_weights, void *y,
+                         int64_t ldy, mx_stream_t stream);
+
+/* ---- Low-rank adapters beside a projection ---- */
+
+/* Workspace bytes mx_lora_add needs (partial products of x and A in fp32). */
+mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t M, size_t *bytes);
+
+/* The adapters of many requests added to a shared projection's output:
+ *   y[m][n] = bf16(base[m][n] + scales[g] sum_r (sum_k x[m][k] A[g][r][k]) B[g][n][r])
+ * with g = ids[m]; y[m] = base[m] where g is outside [0, L).  Sums in fp32, the
+ * inner one kept to 16 significant bits, y rounded once.  Rows in any order.
+ * Adapters of smaller rank are padded with zeros to R.
+ *   a      (device) bf16 [L, R, K], 16-byte aligned
+ *   b      (device) bf16 [L, N, R], 16-byte aligned
+ *   scales (device, nullable: 1) fp32 [L]
+ *   x      (device) bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K: the
+ *          projection's input; rows without an adapter are not read
+ *   ids    (device) int32 [M]
+ *   base   (device) bf16 [M, ldb], 16-byte aligned, ldb % 8 == 0, ldb >= N:
+ *          mx_linear's y
+ *   y      (device) bf16 [M, ldy], the same rules; may be base itself (the same
+ *          pointer and leading dimension)
+ *   ws     (device) mx_lora_workspace's bytes, 16-byte aligned
+ * Rules: L >= 1, R % 8 == 0, 8 <= R <= 256, K % 32 == 0, N % 16 == 0,
+ * 1 <= M <= 4000000; one adapter's A and B and 64 rows of x, base and y stay
+ * below 2 GiB.  Other overlaps of y or ws: MX_ERR_UNSUPPORTED.  Asynchronous,
+ * allocates nothing; calls that share a workspace must be ordered. */
+mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a, const void *b,
+                      const float *scales, int64_t M, const void *x, int64_t ldx,
+                      const int32_t *ids, const void *base, int64_t ldb, void *y, int64_t ldy,
+                      void *ws, size_t ws_bytes, mx_stream_t stream);
+
 /* Batch-invariant mode ([rocm_native] process_weights_after_loading: under
  * VLLM_BATCH_INVARIANT the page leaves its block-scaled GEMM, whose split of
  * K varies with M).  Here the decode GEMVs (every A16 call, W8A8 with

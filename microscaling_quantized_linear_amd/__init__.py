@@ -26,6 +26,9 @@ __all__ = [
     "mx_moe_down", "mx_fold_row_codes", "mx_e4m3_from_dequant", "mx_set_batch_invariant",
     "mx_fused_layout_permute", "MX_PERM_Q_ROWS", "MX_PERM_O_COLS", "mx_status_str",
     "mx_arch_supported",
+    "MX_EPI_NONE", "MX_EPI_SILU", "mx_add_rms_norm", "mx_moe_sort_workspace", "mx_moe_sort",
+    "mx_grouped_workspace", "mx_grouped_linear", "mx_moe_combine", "mx_lora_workspace",
+    "mx_lora_add",
 ]
 
 MX_E4M3, MX_E2M1 = 0, 1
@@ -33,6 +36,7 @@ MX_SCALE_ROW32, MX_SCALE_BLK32 = 0, 1
 MX_RULE_OCP, MX_RULE_CEIL448 = 0, 1
 MX_ACT_BF16, MX_ACT_MXFP8, MX_ACT_MXFP8_T16 = 0, 1, 2
 MX_PERM_Q_ROWS, MX_PERM_O_COLS = 0, 1
+MX_EPI_NONE, MX_EPI_SILU = 0, 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmx.so")
 _lib = None
@@ -87,6 +91,24 @@ def lib() -> C.CDLL:
                      "mx_moe_gate_up", "mx_moe_down",
                      "mx_fold_row_codes", "mx_e4m3_from_dequant", "mx_fused_layout_permute"):
             getattr(L, name).restype = i32
+        f32 = C.c_float
+        for name, args in {
+                "mx_add_rms_norm": [i64, i64, p, i64, p, i64, p, f32, i32, i32, p, i64, p, i64, p,
+                                    i64, p, i64, p],
+                "mx_moe_sort_workspace": [i64, i64, i64, C.POINTER(sz)],
+                "mx_moe_sort": [i64, i64, i64, p, p, p, p, p, sz, p],
+                "mx_grouped_workspace": [i32, i32, i64, i64, i64, i64, i32, i32, C.POINTER(sz)],
+                "mx_grouped_linear": [i32, i32, i64, i64, i64, p, p, i64, p, i32, i32, i64, p, i64,
+                                      p, i64, p, i64, p, i32, p, i64, p, sz, p],
+                "mx_moe_combine": [i64, i64, i64, i64, p, i64, p, p, p, i64, p],
+                "mx_lora_workspace": [i64, i64, i64, i64, i64, C.POINTER(sz)],
+                "mx_lora_add": [i64, i64, i64, i64, p, p, p, i64, p, i64, p, p, i64, p, i64, p, sz,
+                                p]}.items():
+            # a build of part of the sources (the host checks') may lack these;
+            # calling one then raises AttributeError
+            if hasattr(L, name):
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = i32
         _lib = L
     return _lib
 
@@ -228,3 +250,76 @@ def mx_fused_layout_permute(kind, layout, N, K, heads, w, codes, w_out, codes_ou
     _check(lib().mx_fused_layout_permute(kind, layout, N, K, heads, _ptr(w), _ptr(codes),
                                          _ptr(w_out), _ptr(codes_out), _stream(stream)),
            "mx_fused_layout_permute")
+
+
+def _here(*tensors):
+    """Device pointers of tensors that lie on the current device (raw integer
+    pointers and None pass through): a host tensor, or one of another device,
+    is refused before its address reaches a kernel."""
+    current = None
+    out = []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if current is None:
+            import torch
+            current = torch.cuda.current_device() if t.is_cuda else -2
+        if t.get_device() != current:
+            raise ValueError(f"a tensor is on {t.device}, not on the current GPU")
+        out.append(t.data_ptr())
+    return out
+
+
+def mx_add_rms_norm(M, K, x, ldx, residual, ldr, weight, eps, act, rule, sum, lds, y, ldy, xq, ldq,
+                    xcodes, ldc, stream=None):
+    x, residual, weight, sum, y, xq, xcodes = _here(x, residual, weight, sum, y, xq, xcodes)
+    _check(lib().mx_add_rms_norm(M, K, x, ldx, residual, ldr, weight, eps, act, rule, sum, lds, y,
+                                 ldy, xq, ldq, xcodes, ldc, _stream(stream)), "mx_add_rms_norm")
+
+
+def mx_moe_sort_workspace(E, T, topk):
+    b = C.c_size_t()
+    _check(lib().mx_moe_sort_workspace(E, T, topk, C.byref(b)), "mx_moe_sort_workspace")
+    return b.value
+
+
+def mx_moe_sort(E, T, topk, topk_ids, offsets, rows, pos, ws, ws_bytes, stream=None):
+    topk_ids, offsets, rows, pos, ws = _here(topk_ids, offsets, rows, pos, ws)
+    _check(lib().mx_moe_sort(E, T, topk, topk_ids, offsets, rows, pos, ws, ws_bytes,
+                             _stream(stream)), "mx_moe_sort")
+
+
+def mx_grouped_workspace(elem, layout, E, N, K, M, act, prequantized):
+    b = C.c_size_t()
+    _check(lib().mx_grouped_workspace(elem, layout, E, N, K, M, act, int(prequantized),
+                                      C.byref(b)), "mx_grouped_workspace")
+    return b.value
+
+
+def mx_grouped_linear(elem, layout, E, N, K, w_packed, codes_packed, M, offsets, act, rule, xrows,
+                      x, ldx, xq, ldq, xcodes, ldc, rows, epi, y, ldy, ws, ws_bytes, stream=None):
+    w_packed, codes_packed, offsets, x, xq, xcodes, rows, y, ws = _here(
+        w_packed, codes_packed, offsets, x, xq, xcodes, rows, y, ws)
+    _check(lib().mx_grouped_linear(elem, layout, E, N, K, w_packed, codes_packed, M, offsets, act,
+                                   rule, xrows, x, ldx, xq, ldq, xcodes, ldc, rows, epi, y, ldy,
+                                   ws, ws_bytes, _stream(stream)), "mx_grouped_linear")
+
+
+def mx_moe_combine(T, topk, N, M, ys, ldys, pos, topk_weights, y, ldy, stream=None):
+    ys, pos, topk_weights, y = _here(ys, pos, topk_weights, y)
+    _check(lib().mx_moe_combine(T, topk, N, M, ys, ldys, pos, topk_weights, y, ldy,
+                                _stream(stream)), "mx_moe_combine")
+
+
+def mx_lora_workspace(L, R, N, K, M):
+    b = C.c_size_t()
+    _check(lib().mx_lora_workspace(L, R, N, K, M, C.byref(b)), "mx_lora_workspace")
+    return b.value
+
+
+def mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws, ws_bytes,
+                stream=None):
+    a, b, scales, x, ids, base, y, ws = _here(a, b, scales, x, ids, base, y, ws)
+    _check(lib().mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws,
+                             ws_bytes, _stream(stream)), "mx_lora_add")

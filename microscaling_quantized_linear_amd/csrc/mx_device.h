@@ -232,4 +232,40 @@ __device__ inline v4u quant_half_block_cvt(v4u v0, v4u v1, uint32_t &code) {
     return out;
 }
 
+// A quarter of a block per lane: eight bf16 values, the block's other three
+// quarters in the lanes of the same quad.  Returns the eight e4m3 bytes and
+// the block's code; the same bytes as quant_half_block.
+template <int RULE>
+__device__ inline v2u quant_eighth(v4u v, uint32_t &code) {
+    u16x2 m = __builtin_bit_cast(u16x2, v[0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
+    uint32_t amax = (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+    // DPP quad_perm [1,0,3,2] then [2,3,0,1]: max over the 4 lanes of a quad
+    uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, true);
+    amax = amax > o ? amax : o;
+    o = (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, true);
+    amax = amax > o ? amax : o;
+    code = act_code<RULE>(amax);
+    const float scale = __uint_as_float(code << 23);
+    v2u out;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        // copies: a bit cast of a vector's element reads the vector's start
+        const uint32_t lo = v[2 * d], hi = v[2 * d + 1];
+        v2s r = {0, 0};
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(v2bf, lo), scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(v2bf, hi), scale, true);
+        uint32_t w = __builtin_bit_cast(uint32_t, r);
+        if (RULE == 0) {
+            // a quotient that rounds above 448 comes out as NaN: 0x7F / 0xFF -> 0x7E / 0xFE
+            const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            w -= nan >> 7;
+        }
+        out[d] = w;
+    }
+    return out;
+}
+
 }  // namespace mx

@@ -148,4 +148,87 @@ inline int64_t act_t16_data_bytes(int64_t M, int64_t K) {
     return (M + 15) / 16 * ((K + 127) / 128) * 2048;
 }
 
+// ---- the operators around the linear (mx_ops_api.cpp) ----
+
+constexpr int64_t kMaxRows = 4000000;      // a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxLd = int64_t(1) << 30;
+constexpr int64_t kMaxT16Bytes = int64_t(1) << 38;   // the same, one wavefront per 8 KB staged
+constexpr int64_t kMaxExperts = 65535;     // one launch-grid row each
+
+// Residual addition, RMS norm and quantization (mx_norm.hip); null pointers
+// switch the residual, the stored sum, the bf16 output off.
+struct NormArgs {
+    int64_t M, K;
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *res;
+    int64_t ldr;
+    const uint16_t *weight;
+    float eps;
+    uint16_t *sum;
+    int64_t lds;
+    uint16_t *y;
+    int64_t ldy;
+    uint8_t *xq;
+    int64_t ldq;
+    uint8_t *xcodes;
+    int64_t ldc;
+};
+constexpr int64_t kNormMaxK = 65536;       // eight wavefronts of 16 segments of 512 values
+hipError_t launch_add_rms_norm(const NormArgs &a, int act, int rule, hipStream_t stream);
+
+// Routed pairs in expert order (mx_route.hip).
+constexpr int64_t kSortMaxExperts = 1024;
+int64_t moe_sort_ws_bytes(int64_t E, int64_t pairs);
+hipError_t launch_moe_sort(int64_t E, int64_t pairs, int64_t topk, const int32_t *ids,
+                           int32_t *offsets, int32_t *rows, int32_t *pos, void *ws,
+                           hipStream_t stream);
+hipError_t launch_moe_gather_sum(int64_t T, int64_t topk, int64_t N, int64_t M, const uint16_t *ys,
+                                 int64_t ldys, const int32_t *pos, const float *wts, uint16_t *y,
+                                 int64_t ldy, hipStream_t stream);
+
+// Products grouped by expert over ragged row ranges (mx_grouped.hip).
+struct GroupedArgs {
+    const uint8_t *w, *codes;      // packed weights and codes of E experts
+    int64_t E, N, K;
+    int64_t M;                     // rows of y and of the T16 activation
+    const int32_t *offsets;        // [E + 1] row ranges
+    const uint8_t *xq, *xct;       // T16 activation of M rows
+    uint16_t *y;
+    int64_t ldy;
+    int epi;                       // 1 = silu(row 2i) * row 2i+1 -> output i (width N / 2)
+};
+hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t stream);
+const char *grouped_kernel_name(const GroupedArgs &a);   // for the dispatch trace
+// T16 activation of M rows, row i taken from source row rows[i] (rows null: i),
+// for i < offsets[E]: from bf16 (quantized with `rule`) or row-major MXFP8
+struct StageArgs {
+    int64_t M, K, E, xrows;
+    const int32_t *offsets, *rows;
+    const uint16_t *x;             // bf16, or null
+    int64_t ldx;
+    const uint8_t *xq, *xc;        // row-major MXFP8
+    int64_t ldq, ldc;
+    uint8_t *out, *outc;
+};
+hipError_t launch_stage_rows(const StageArgs &a, int rule, hipStream_t stream);
+
+// Low-rank adapters beside a projection (mx_lora.hip).
+struct LoraArgs {
+    int64_t L, R, N, K, M;
+    const uint16_t *a, *b;
+    const float *scales;
+    const uint16_t *x;
+    int64_t ldx;
+    const int32_t *ids;
+    const uint16_t *base;
+    int64_t ldb;
+    uint16_t *y;
+    int64_t ldy;
+    float *ws;                     // [splits][M][R] partial products x A^T
+};
+constexpr int64_t kLoraMaxRank = 256;
+int64_t lora_splits(int64_t M, int64_t K);
+hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
+
 }  // namespace mx
