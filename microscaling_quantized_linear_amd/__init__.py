@@ -256,26 +256,45 @@ def _here(*tensors):
     """Device pointers of tensors that lie on the current device (raw integer
     pointers and None pass through): a host tensor, or one of another device,
     is refused before its address reaches a kernel."""
-    current = None
+    current = -2
     out = []
     for t in tensors:
-        if t is None or isinstance(t, int):
-            out.append(t)
-            continue
-        if current is None:
-            import torch
-            current = torch.cuda.current_device() if t.is_cuda else -2
-        if t.get_device() != current:
-            raise ValueError(f"a tensor is on {t.device}, not on the current GPU")
-        out.append(t.data_ptr())
+        if t is not None and not isinstance(t, int):
+            at = t.get_device()
+            if current == -2 and at >= 0:
+                current = _torch_c()._cuda_getDevice()
+            if at != current:
+                raise ValueError(f"a tensor is on {t.device}, not on the current GPU")
+            t = t.data_ptr()
+        out.append(t)
     return out
+
+
+_C = None
+
+
+def _torch_c():
+    global _C
+    if _C is None:
+        import torch
+        _C = torch._C
+    return _C
+
+
+def _raw_stream(stream):
+    """As _stream, without making a stream object of the current stream: a
+    decode step makes these calls every few microseconds."""
+    if stream is None:
+        c = _torch_c()
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _stream(stream)
 
 
 def mx_add_rms_norm(M, K, x, ldx, residual, ldr, weight, eps, act, rule, sum, lds, y, ldy, xq, ldq,
                     xcodes, ldc, stream=None):
     x, residual, weight, sum, y, xq, xcodes = _here(x, residual, weight, sum, y, xq, xcodes)
     _check(lib().mx_add_rms_norm(M, K, x, ldx, residual, ldr, weight, eps, act, rule, sum, lds, y,
-                                 ldy, xq, ldq, xcodes, ldc, _stream(stream)), "mx_add_rms_norm")
+                                 ldy, xq, ldq, xcodes, ldc, _raw_stream(stream)), "mx_add_rms_norm")
 
 
 def mx_moe_sort_workspace(E, T, topk):
@@ -287,7 +306,7 @@ def mx_moe_sort_workspace(E, T, topk):
 def mx_moe_sort(E, T, topk, topk_ids, offsets, rows, pos, ws, ws_bytes, stream=None):
     topk_ids, offsets, rows, pos, ws = _here(topk_ids, offsets, rows, pos, ws)
     _check(lib().mx_moe_sort(E, T, topk, topk_ids, offsets, rows, pos, ws, ws_bytes,
-                             _stream(stream)), "mx_moe_sort")
+                             _raw_stream(stream)), "mx_moe_sort")
 
 
 def mx_grouped_workspace(elem, layout, E, N, K, M, act, prequantized):
@@ -303,13 +322,13 @@ def mx_grouped_linear(elem, layout, E, N, K, w_packed, codes_packed, M, offsets,
         w_packed, codes_packed, offsets, x, xq, xcodes, rows, y, ws)
     _check(lib().mx_grouped_linear(elem, layout, E, N, K, w_packed, codes_packed, M, offsets, act,
                                    rule, xrows, x, ldx, xq, ldq, xcodes, ldc, rows, epi, y, ldy,
-                                   ws, ws_bytes, _stream(stream)), "mx_grouped_linear")
+                                   ws, ws_bytes, _raw_stream(stream)), "mx_grouped_linear")
 
 
 def mx_moe_combine(T, topk, N, M, ys, ldys, pos, topk_weights, y, ldy, stream=None):
     ys, pos, topk_weights, y = _here(ys, pos, topk_weights, y)
     _check(lib().mx_moe_combine(T, topk, N, M, ys, ldys, pos, topk_weights, y, ldy,
-                                _stream(stream)), "mx_moe_combine")
+                                _raw_stream(stream)), "mx_moe_combine")
 
 
 def mx_lora_workspace(L, R, N, K, M):
@@ -322,4 +341,4 @@ def mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws,
                 stream=None):
     a, b, scales, x, ids, base, y, ws = _here(a, b, scales, x, ids, base, y, ws)
     _check(lib().mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws,
-                             ws_bytes, _stream(stream)), "mx_lora_add")
+                             ws_bytes, _raw_stream(stream)), "mx_lora_add")

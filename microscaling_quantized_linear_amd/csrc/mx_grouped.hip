@@ -21,6 +21,8 @@
 #include "mx_device.h"
 #include "mx_kernels.h"
 
+#include <cstdlib>
+
 namespace mx {
 
 constexpr int kStreamWaves = 4;
@@ -178,9 +180,30 @@ static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-const char *grouped_kernel_name(const GroupedArgs &) { return "grouped_stream_kernel"; }
+// Which form serves a call: 0 streams the weights, 1 and 2 are the tiled form
+// with 128- and 256-row tiles.  MX_GROUPED_FORM (1 to 3) overrides the rule
+// (tuning sweeps only; read once).
+static int grouped_form(const GroupedArgs &a) {
+    static const int forced = [] {
+        const char *s = std::getenv("MX_GROUPED_FORM");
+        return s ? std::atoi(s) : 0;
+    }();
+    if (forced >= 1 && forced <= 3) return forced - 1;
+    const int64_t rows = a.M / a.E;                       // an expert's rows, on average
+    const int64_t panels = a.E * ((a.N + 255) / 256);
+    if (rows <= (panels < 128 ? 96 : 6)) return 0;
+    return panels * ((rows + 255) / 256) >= 512 ? 2 : 1;
+}
+
+const char *grouped_kernel_name(const GroupedArgs &a) {
+    const int form = grouped_form(a);
+    return form == 0   ? "grouped_stream_kernel"
+           : form == 1 ? "grouped_gemm_kernel 128-row tiles"
+                       : "grouped_gemm_kernel 256-row tiles";
+}
 
 hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t st) {
+    if (const int mt = grouped_form(a)) return launch_grouped_gemm(elem, layout, mt, a, st);
     if (elem == E2M1) return launch_stream<E2M1, ROW32>(a, st);
     return layout == ROW32 ? launch_stream<E4M3, ROW32>(a, st) : launch_stream<E4M3, BLK32>(a, st);
 }
