@@ -332,6 +332,10 @@ __global__ void __launch_bounds__(256, 1) grouped_gemm_kernel(GroupedArgs p) {
         }
     }
 
+    // the copies of zeros behind the last step have landed too: none outlives
+    // the workgroup
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+
     // ---- epilogue: element i of lane (g, rr) in tile (nt, mt) is weight row
     // 32 nt + 8 (i / 4) + 4 g + i % 4 and row 32 mt + rr.  Pairs are rounded
     // together, v_permlane32_swap trades pieces between lanes rr and rr + 32,

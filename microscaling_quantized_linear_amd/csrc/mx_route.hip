@@ -45,15 +45,24 @@ __device__ inline int expert_of(const int32_t *ids, int64_t i, int64_t end, int 
 }
 
 // Histogram of each wavefront's pairs in cnt[wave][0 .. E]: wavefront w of
-// part [first, end) takes the `per` pairs from first + w * per on.
+// part [first, end) takes the `per` pairs from first + w * per on.  The experts
+// of its first kKept groups of 64 pairs stay in `kept`.
+constexpr int kKept = 4;
 __device__ inline void count_part(const int32_t *ids, int64_t first, int64_t end, int64_t per,
-                                  int E, int *cnt, int bins) {
+                                  int E, int *cnt, int bins, int (&kept)[kKept]) {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t at = first + wave * per + lane;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) kept[i] = 64 * i < per ? expert_of(ids, at + 64 * i, end, E) : -1;
     for (int b = threadIdx.x; b < kSortWaves * bins; b += kSortThreads) cnt[b] = 0;
     __syncthreads();
-    for (int64_t i = 0; i < per; i += 64) {
-        const int e = expert_of(ids, first + wave * per + i + lane, end, E);
-        if (e >= 0) atomicAdd(&cnt[wave * bins + e], 1);  // whole numbers: no order in the sum
+    // whole numbers: the order of the additions does not show
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (kept[i] >= 0) atomicAdd(&cnt[wave * bins + kept[i]], 1);
+    for (int64_t i = 64 * kKept; i < per; i += 64) {
+        const int e = expert_of(ids, at + i, end, E);
+        if (e >= 0) atomicAdd(&cnt[wave * bins + e], 1);
     }
     __syncthreads();
 }
@@ -63,7 +72,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(
     extern __shared__ int cnt[];
     const int bins = E + 1;
     const int64_t first = blockIdx.x * part, end = first + part < pairs ? first + part : pairs;
-    count_part(ids, first, end, part / kSortWaves, E, cnt, bins);
+    int kept[kKept];
+    count_part(ids, first, end, part / kSortWaves, E, cnt, bins, kept);
     for (int b = threadIdx.x; b < bins; b += kSortThreads) {
         int n = 0;
         for (int w = 0; w < kSortWaves; ++w) n += cnt[w * bins + b];
@@ -77,31 +87,43 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
     const int32_t *__restrict__ ids, int64_t pairs, int64_t part, int E, int topk, int bits,
     const int32_t *__restrict__ hist, int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
     int32_t *__restrict__ pos) {
-    extern __shared__ int cnt[];                          // [waves][bins], then total[bins]
+    extern __shared__ int cnt[];                          // [waves][bins], total[bins], base[bins]
     __shared__ int wsum[kSortWaves];
     const int bins = E + 1;
-    int *total = cnt + kSortWaves * bins;
+    int *total = cnt + kSortWaves * bins, *base = total + bins;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t first = blockIdx.x * part, end = first + part < pairs ? first + part : pairs;
     const int64_t per = part / kSortWaves;
-    count_part(ids, first, end, per, E, cnt, bins);
-    // total[b]: every part's pairs of expert b; cnt[w][b]: those in earlier
-    // parts and in earlier wavefronts of this one
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-        int before = 0, all = 0;
-        if (hist) {
-            for (int q = 0; q < (int)gridDim.x; ++q) {
+    int kept[kKept];
+    // total[b]: every part's pairs of expert b; base[b]: those in earlier parts.
+    // Several threads share an expert's parts where the experts are few.
+    for (int b = threadIdx.x; b < 2 * bins; b += kSortThreads) total[b] = 0;
+    count_part(ids, first, end, per, E, cnt, bins, kept);
+    if (hist) {
+        const int teams = kSortThreads / bins > 0 ? kSortThreads / bins : 1;
+        for (int i = threadIdx.x; i < teams * bins; i += kSortThreads) {
+            const int b = i % bins, parts = (int)gridDim.x;
+            int before = 0, all = 0;
+#pragma unroll 8
+            for (int q = i / bins; q < parts; q += teams) {
                 const int n = hist[(int64_t)q * bins + b];
                 before += q < (int)blockIdx.x ? n : 0;
                 all += n;
             }
+            atomicAdd(&total[b], all);
+            atomicAdd(&base[b], before);
         }
+        __syncthreads();
+    }
+    // cnt[w][b]: the pairs of expert b ahead of wavefront w's
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+        int before = base[b];
         for (int w = 0; w < kSortWaves; ++w) {
             const int n = cnt[w * bins + b];
             cnt[w * bins + b] = before;
             before += n;
         }
-        total[b] = hist ? all : before;
+        if (!hist) total[b] = before;
     }
     __syncthreads();
     // exclusive sums of total over the experts, 512 bins at a time
@@ -130,9 +152,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
         for (int b = threadIdx.x; b < bins; b += kSortThreads) offsets[b] = total[b];
     // the pairs, 64 of a wavefront at a time and in order
     int *mine = cnt + wave * bins;
-    for (int64_t i = 0; i < per; i += 64) {
-        const int64_t pair = first + wave * per + i + lane;
-        const int e = expert_of(ids, pair, end, E);
+    auto put = [&](int e, int64_t pair) {
         uint64_t same = __ballot(e >= 0);
         for (int bit = 0; bit < bits; ++bit) {
             const uint64_t on = __ballot(e >> bit & 1);
@@ -143,7 +163,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
             const int at = mine[e] + rank;
             __builtin_amdgcn_wave_barrier();
             const int place = total[e] + at;
-            rows[place] = e < E ? (int32_t)(pair / topk) : -1;
+            rows[place] = e < E ? (int32_t)((uint32_t)pair / (uint32_t)topk) : -1;
             pos[pair] = e < E ? place : -1;
             // the last lane of the expert moves its count on, once every lane
             // of the wavefront has read it (LDS operations of a wavefront
@@ -151,7 +171,11 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
             if (rank == __popcll(same) - 1) mine[e] = at + 1;
         }
         __builtin_amdgcn_wave_barrier();
-    }
+    };
+    const int64_t at = first + wave * per + lane;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) put(kept[i], at + 64 * i);
+    for (int64_t i = 64 * kKept; i < per; i += 64) put(expert_of(ids, at + i, end, E), at + i);
 }
 
 hipError_t launch_moe_sort(int64_t E, int64_t pairs, int64_t topk, const int32_t *ids,
@@ -168,7 +192,8 @@ hipError_t launch_moe_sort(int64_t E, int64_t pairs, int64_t topk, const int32_t
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)n), dim3(kSortThreads), lds + bins * 4, st,
+    hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)n), dim3(kSortThreads), lds + 2 * bins * 4,
+                       st,
                        ids, pairs, part, (int)E, (int)topk, bits, hist, offsets, rows, pos);
     return hipGetLastError();
 }
