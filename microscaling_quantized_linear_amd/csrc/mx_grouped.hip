@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves) grouped_stream_kernel(Group
             const uint32_t past = s < s1 ? 0u : kOOB;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const uint32_t o = 16u * lane, base = (uint32_t)(t * TILEB + (int64_t)s * CHUNK) & ~kOOB;
+                const uint32_t o = 16u * lane;
+                const uint32_t base = (uint32_t)(t * TILEB + (int64_t)s * CHUNK) & ~kOOB;
                 const bool last = s == S - 1;
                 st.w0[t] = load16<kNT>(wr, (base + o) | past | (last && o >= tailb ? kOOB : 0u));
                 if (ELEM == E4M3)
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves) grouped_stream_kernel(Group
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const uint32_t off = (xo[i] & ~kOOB) + (uint32_t)s * 2048u, bad = (xo[i] & kOOB) | past;
+                const uint32_t off = (xo[i] & ~kOOB) + (uint32_t)s * 2048u;
+                const uint32_t bad = (xo[i] & kOOB) | past;
                 st.x0[i] = load16(xr, off | bad);
                 st.x1[i] = load16(xr, (off + 1024u) | bad);
                 st.cx[i] = load4(xcr, ((xco[i] & ~kOOB) + (uint32_t)(s / 4) * 256u) | bad);
@@ -181,18 +183,31 @@ static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
 }
 
 // Which form serves a call: 0 streams the weights, 1 and 2 are the tiled form
-// with 128- and 256-row tiles.  MX_GROUPED_FORM (1 to 3) overrides the rule
-// (tuning sweeps only; read once).
+// with tiles of up to 128 and 256 rows.  The host knows the rows' number, not
+// their split: the rule goes by the average.  Measured (us, streaming / 128 /
+// 256; e4m3 unless named):
+//   an expert's rows      4            8            16           128
+//   E 32, 4096 x 4096     82/92/92     93/95/95     100/96/96    394/126/114
+//   the same, e2m1        51/52/53     62/55/55     66/55/56     273/87/81
+//   E 24, 4096 x 1568     24/30/30                  43/31/31
+//   E 64, 512 x 2048      14/17/17                  23/18/18     89/22/28
+// and with fewer weight panels (of 256 rows) than half the compute units, where
+// the tiled form leaves the others idle:
+//   an expert's rows      64           128          256          1024       4096
+//   E 1, 4096 x 4096      10/23/23     20/23/23     36/24/39     142/28/42  557/66/59
+//   E 8, 1024 x 1024      6/10/10      9/11/11                   (512: 33/13/18)
+// MX_GROUPED_FORM (1 to 3) overrides the rule (tuning sweeps only; read once).
 static int grouped_form(const GroupedArgs &a) {
     static const int forced = [] {
         const char *s = std::getenv("MX_GROUPED_FORM");
         return s ? std::atoi(s) : 0;
     }();
+    if (a.E > kGroupedMaxExperts) return 0;
     if (forced >= 1 && forced <= 3) return forced - 1;
     const int64_t rows = a.M / a.E;                       // an expert's rows, on average
     const int64_t panels = a.E * ((a.N + 255) / 256);
-    if (rows <= (panels < 128 ? 96 : 6)) return 0;
-    return panels * ((rows + 255) / 256) >= 512 ? 2 : 1;
+    if (rows <= (panels < 128 ? 128 : 6)) return 0;
+    return rows >= 128 && panels * ((rows + 255) / 256) >= 256 ? 2 : 1;
 }
 
 const char *grouped_kernel_name(const GroupedArgs &a) {
@@ -203,7 +218,8 @@ const char *grouped_kernel_name(const GroupedArgs &a) {
 }
 
 hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t st) {
-    if (const int mt = grouped_form(a)) return launch_grouped_gemm(elem, layout, mt, a, st);
+    if (const int form = grouped_form(a))
+        return launch_grouped_gemm(elem, layout, 128 * form, a, st);
     if (elem == E2M1) return launch_stream<E2M1, ROW32>(a, st);
     return layout == ROW32 ? launch_stream<E4M3, ROW32>(a, st) : launch_stream<E4M3, BLK32>(a, st);
 }

@@ -200,8 +200,9 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t stream);
 const char *grouped_kernel_name(const GroupedArgs &a);   // for the dispatch trace
-// the tiled form (mx_grouped_gemm.hip): mt 32-row slabs a wavefront (1 or 2)
-hipError_t launch_grouped_gemm(int elem, int layout, int mt, const GroupedArgs &a,
+// the tiled form (mx_grouped_gemm.hip): tiles of up to bm rows (128 or 256)
+constexpr int64_t kGroupedMaxExperts = 1024;   // whose tile counts it keeps in LDS
+hipError_t launch_grouped_gemm(int elem, int layout, int bm, const GroupedArgs &a,
                                hipStream_t stream);
 // T16 activation of M rows, row i taken from source row rows[i] (rows null: i),
 // for i < offsets[E]: from bf16 (quantized with `rule`) or row-major MXFP8

@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
                 for (int w = 1; w < kShrinkWaves; ++w) s += red[w][i][l];
                 const int row = 16 * i + l % 16, rank = rank0 + 16 * t + 4 * (l / 16);
                 if ((same >> row & 1) && rank < Rp)
-                    *reinterpret_cast<v4f *>(p.ws + ((int64_t)split * p.M + m0 + row) * Rp + rank) = s;
+                    *reinterpret_cast<v4f *>(p.ws + ((int64_t)split * p.M + m0 + row) * Rp +
+                                             rank) = s;
             }
             __syncthreads();
         }
@@ -310,8 +311,9 @@ __global__ void __launch_bounds__(256) lora_shrink_tiled_kernel(LoraArgs p, int 
 // NC: chunks of 32 ranks whose columns of B are loaded together.  STAGED: B's
 // rows of the workgroup's columns go through LDS, in whole lines and once for
 // both row groups; the operand-shaped loads (64 bytes of 16 rows, 8 R apart)
-// cost 20 of 47 us at R = 64, N = 4096, M = 4096.  The tile's rows are shared out to RG groups of wavefronts, 16 MW rows each, and a
-// workgroup covers 128 columns for every wavefront of a group.
+// cost 20 of 47 us at R = 64, N = 4096, M = 4096.  The tile's rows are shared out
+// to RG groups of wavefronts, 16 MW rows each, and a workgroup covers 128 columns
+// for every wavefront of a group.
 template <int MT, int NC, bool STAGED>
 __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(LoraArgs p, int splits,
                                                                             int shares) {

@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
         v4u o;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-            const float lo = __uint_as_float(v[i][d] << 16) * scale * __uint_as_float(wt[i][d] << 16);
+            const float lo = __uint_as_float(v[i][d] << 16) * scale *
+                             __uint_as_float(wt[i][d] << 16);
             const float hi = __uint_as_float(v[i][d] & 0xFFFF0000u) * scale *
                              __uint_as_float(wt[i][d] & 0xFFFF0000u);
             o[d] = live ? bf16_bits(lo) | bf16_bits(hi) << 16 : 0u;   // padding rows: +0

@@ -53,7 +53,8 @@ __device__ inline void count_part(const int32_t *ids, int64_t first, int64_t end
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t at = first + wave * per + lane;
 #pragma unroll
-    for (int i = 0; i < kKept; ++i) kept[i] = 64 * i < per ? expert_of(ids, at + 64 * i, end, E) : -1;
+    for (int i = 0; i < kKept; ++i)
+        kept[i] = 64 * i < per ? expert_of(ids, at + 64 * i, end, E) : -1;
     for (int b = threadIdx.x; b < kSortWaves * bins; b += kSortThreads) cnt[b] = 0;
     __syncthreads();
     // whole numbers: the order of the additions does not show
@@ -68,7 +69,8 @@ __device__ inline void count_part(const int32_t *ids, int64_t first, int64_t end
 }
 
 __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(
-    const int32_t *__restrict__ ids, int64_t pairs, int64_t part, int E, int32_t *__restrict__ hist) {
+    const int32_t *__restrict__ ids, int64_t pairs, int64_t part, int E,
+    int32_t *__restrict__ hist) {
     extern __shared__ int cnt[];
     const int bins = E + 1;
     const int64_t first = blockIdx.x * part, end = first + part < pairs ? first + part : pairs;
@@ -193,8 +195,7 @@ hipError_t launch_moe_sort(int64_t E, int64_t pairs, int64_t topk, const int32_t
         if (err != hipSuccess) return err;
     }
     hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)n), dim3(kSortThreads), lds + 2 * bins * 4,
-                       st,
-                       ids, pairs, part, (int)E, (int)topk, bits, hist, offsets, rows, pos);
+                       st, ids, pairs, part, (int)E, (int)topk, bits, hist, offsets, rows, pos);
     return hipGetLastError();
 }
 

@@ -261,7 +261,7 @@ def run_grouped(g, mx, elem, layout, E, N, K, packed, offsets, M, x=None, given=
     y = out16(g, M + 1, ldy)
     act = T16 if t16 is not None else MXFP8
     need = mx.mx_grouped_workspace(elem, layout, E, N, K, M, act, given is not None)
-    ws = bytes_(g, max(need, 16), fill=0x7F)          # NaN bytes: what is not staged must not be read
+    ws = bytes_(g, max(need, 16), fill=0x7F)          # NaN bytes: unstaged ones must not be read
     off, rd = g.dev(np.asarray(offsets, np.int32)), g.dev(rows) if rows is not None else None
     kw = dict(xd=None, ldx=0, q=None, ldq=0, c=None, ldc=0, xrows=0)
     if t16 is not None:
@@ -545,7 +545,8 @@ class Layer:
         self.d_w, self.d_c, self.dn = weight(g, r, 0, 0, E, H, I, 114, 120)
         self.a, self.b, self.s, _, self.aid, _ = lora_inputs(r, L, R, N, H, T, "mixed")
         d = g.dev
-        self.d = {k: d(getattr(self, k)) for k in ("x", "res", "w", "ids", "wts", "a", "b", "s", "aid")}
+        self.d = {k: d(getattr(self, k))
+                  for k in ("x", "res", "w", "ids", "wts", "a", "b", "s", "aid")}
         P = T * topk
         i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=g.DEV)  # noqa: E731
         self.sum, self.h = out16(g, T, H), out16(g, T, H)
@@ -575,8 +576,8 @@ class Layer:
         P = T * topk
         mx.mx_grouped_linear(1, 0, E, 2 * I, H, *self.gu, P, self.off, MXFP8, 0, T, None, 0, self.q,
                              H, self.c, H // 32, self.rows, 1, self.hid, I, ws, n)
-        mx.mx_grouped_linear(0, 0, E, H, I, *self.dn, P, self.off, MXFP8, 0, P, self.hid, I, None, 0,
-                             None, 0, None, 0, self.ys, H, ws, n)
+        mx.mx_grouped_linear(0, 0, E, H, I, *self.dn, P, self.off, MXFP8, 0, P, self.hid, I, None,
+                             0, None, 0, None, 0, self.ys, H, ws, n)
         mx.mx_moe_combine(T, topk, H, P, self.ys, H, self.pos, d["wts"], self.out, H)
 
     def outputs(self):

@@ -132,7 +132,8 @@ REFUSED = [
 ]
 # calls that are in order: refused only for want of a device
 VALID = [
-    (norm, [dict(), dict(act=0), dict(act=0, xq=None, xc=None), dict(act=2), dict(act=2, ldq=0, ldc=0),
+    (norm, [dict(), dict(act=0), dict(act=0, xq=None, xc=None), dict(act=2),
+            dict(act=2, ldq=0, ldc=0),
             dict(res=None, ldr=0), dict(sum=None, lds=0), dict(y=None, ldy=0), dict(sum=A(0)),
             dict(sum=A(1)), dict(sum=A(1), y=A(0)), dict(xc=A(6) + 1), dict(eps=0.0),
             dict(K=65536, ldx=65536, ldr=65536, lds=65536, ldy=65536, ldq=65536, ldc=2048),
@@ -172,7 +173,8 @@ def test_workspaces():
     for M, K in ((1, 32), (17, 160), (300, 1568)):
         qb, cb = mx.mx_act_t16_sizes(M, K)
         for given in (0, 1):
-            assert mx.mx_grouped_workspace(0, 0, 4, 64, K, M, 1, given) == (qb + 255) // 256 * 256 + cb
+            need = mx.mx_grouped_workspace(0, 0, 4, 64, K, M, 1, given)
+            assert need == (qb + 255) // 256 * 256 + cb
         assert mx.mx_grouped_workspace(1, 0, 4, 64, K, M, 2, 1) == 0
     # at least one fp32 partial product per row and rank, ranks padded to 16
     for M, R, K in ((1, 8, 32), (16, 16, 7168), (4096, 72, 7168)):
