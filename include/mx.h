@@ -395,7 +395,7 @@ mx_status mx_moe_down(int elem, int64_t E, int64_t H, int64_t inter,
  *   x        (device) bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K
  *   residual (device, nullable) bf16 [M, ldr], the same rules
  *   weight   (device) bf16 [K], 16-byte aligned
- *   eps      >= 0
+ *   eps      >= 0 (0 makes a row of zeros NaN)
  *   sum      (device, nullable) bf16 [M, lds]: receives s; may be x or residual
  *            itself (the same pointer and leading dimension)
  *   y        (device; nullable unless act is MX_ACT_BF16) bf16 [M, ldy]; may be x
@@ -435,7 +435,8 @@ mx_status mx_moe_sort_workspace(int64_t E, int64_t T, int64_t topk, size_t *byte
  *            expert
  *   ws       (device) at least mx_moe_sort_workspace's bytes, 16-byte aligned
  *            (may be NULL when that is 0)
- * The result is the same in every run.
+ * The result is the same in every run; calls that share a workspace must be
+ * ordered.
  * Rules: 1 <= E <= 1024, T >= 1, 1 <= topk <= E, T * topk <= 4000000; the
  * buffers must not overlap (MX_ERR_UNSUPPORTED). */
 mx_status mx_moe_sort(int64_t E, int64_t T, int64_t topk, const int32_t *topk_ids,
@@ -460,8 +461,9 @@ mx_status mx_grouped_workspace(int elem, int layout, int64_t E, int64_t N, int64
  * (and before offsets[0]) are left as they were.
  *   w_packed, codes_packed (device) from mx_pack_weights(elem, layout, E, N, K)
  *   M        rows of y, at least offsets[E]
- *   offsets  (device) int32 [E + 1], not descending, within 0 .. M (mx_moe_sort's);
- *            what lies outside is cut off
+ *   offsets  (device) int32 [E + 1], within 0 .. M and not descending
+ *            (mx_moe_sort's); what lies outside 0 .. M is cut off, and with
+ *            offsets that descend which rows are written is unspecified
  *   act MX_ACT_MXFP8: row i's activation is source row rows[i] (rows NULL: i,
  *       then xrows >= M); a source row outside [0, xrows) counts as zeros.
  *     x      (device) bf16 [xrows, ldx], 16-byte aligned, ldx % 8 == 0:
@@ -480,7 +482,9 @@ mx_status mx_grouped_workspace(int elem, int layout, int64_t E, int64_t N, int64
  * 128) and 256 rows of y stay below 2 GiB, the staged activation below 256 GiB
  * (MX_ERR_SHAPE).
  * Asynchronous, allocates nothing, may be captured in a graph; calls that share
- * a workspace must be ordered. */
+ * a workspace must be ordered.  The order of summation of an output depends on
+ * M, E and N too (two kernels serve the op), unless the batch-invariant mode is
+ * on: then it is fixed by K alone, at the decode kernel's speed. */
 mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t K,
                             const void *w_packed, const void *codes_packed, int64_t M,
                             const int32_t *offsets, int act, int rule, int64_t xrows,
@@ -495,7 +499,8 @@ mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t 
  *   pos (device) int32 [T, topk] (mx_moe_sort's)
  *   topk_weights (device) fp32 [T, topk]
  *   y   (device) bf16 [T, ldy], 16-byte aligned, ldy % 8 == 0, ldy >= N
- * Rules: T, topk, M >= 1, T * topk and M <= 4000000, N % 8 == 0; y overlaps no
+ * Rules: T, topk, M >= 1, T * topk and M <= 4000000, N % 8 == 0,
+ * N <= 134215680; y overlaps no
  * input (MX_ERR_UNSUPPORTED). */
 mx_status mx_moe_combine(int64_t T, int64_t topk, int64_t N, int64_t M, const void *ys,
                          int64_t ldys, const int32_t *pos, const float *topk_weights, void *y,
@@ -524,8 +529,10 @@ mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t 
  *   ws     (device) mx_lora_workspace's bytes, 16-byte aligned
  * Rules: L >= 1, R % 8 == 0, 8 <= R <= 256, K % 32 == 0, N % 16 == 0,
  * 1 <= M <= 4000000; one adapter's A and B and 64 rows of x, base and y stay
- * below 2 GiB.  Other overlaps of y or ws: MX_ERR_UNSUPPORTED.  Asynchronous,
- * allocates nothing; calls that share a workspace must be ordered. */
+ * below 2 GiB; N <= 16776960, K <= 2^26.  Other overlaps of y or ws:
+ * MX_ERR_UNSUPPORTED.  Asynchronous, allocates nothing; calls that share a
+ * workspace must be ordered.  The order of summation changes at M = 512, unless
+ * the batch-invariant mode is on (it changes the workspace's size too). */
 mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a, const void *b,
                       const float *scales, int64_t M, const void *x, int64_t ldx,
                       const int32_t *ids, const void *base, int64_t ldb, void *y, int64_t ldy,

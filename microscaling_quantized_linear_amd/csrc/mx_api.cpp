@@ -19,6 +19,13 @@ namespace {
 // state, valid before any constructor runs), 1 not gfx950, 2 gfx950
 std::atomic<int> g_arch[64];
 
+// Batch-invariant mode: every W8A8 M runs on the decode GEMV, whose order of
+// summation for an output depends on K alone, so a row's result does not
+// depend on how many rows share the call (the GEMM above kGemvMaxM sums in
+// another order).  Process-wide; MX_BATCH_INVARIANT=1 sets it at start-up and
+// mx_set_batch_invariant changes it.
+std::atomic<int> g_invariant{-1};
+
 // Dispatch trace: with MX_LOG=1 in the environment (read once per process)
 // every launch decision of the hot path goes to stderr as one line: entry
 // point, kernel and its launch plan, and the shape.  Off by default; no
@@ -56,6 +63,17 @@ mx_status device_ok() {
     return ok ? MX_OK : MX_ERR_DEVICE;
 }
 
+bool batch_invariant() {
+    int v = g_invariant.load(std::memory_order_relaxed);
+    if (v < 0) {
+        const char *s = std::getenv("MX_BATCH_INVARIANT");
+        int unset = -1;
+        g_invariant.compare_exchange_strong(unset, s && s[0] && s[0] != '0' ? 1 : 0);
+        v = g_invariant.load(std::memory_order_relaxed);
+    }
+    return v == 1;
+}
+
 void log_dispatch(const char *fmt, ...) {
     if (!log_on()) return;
     char buf[256];
@@ -71,6 +89,7 @@ void log_dispatch(const char *fmt, ...) {
 namespace {
 
 using mx::aligned16;
+using mx::batch_invariant;
 using mx::device_ok;
 using mx::kMaxRsrc;
 using mx::launched;
@@ -89,22 +108,6 @@ using mx::ROW32;
 // largest M served by the decode GEMV for W8A8; above it the GEMM runs
 constexpr int64_t kGemvMaxM = 64;
 
-// Batch-invariant mode: every W8A8 M runs on the decode GEMV, whose order of
-// summation for an output depends on K alone, so a row's result does not
-// depend on how many rows share the call (the GEMM above kGemvMaxM sums in
-// another order).  Process-wide; MX_BATCH_INVARIANT=1 sets it at start-up and
-// mx_set_batch_invariant changes it.
-std::atomic<int> g_invariant{-1};
-bool batch_invariant() {
-    int v = g_invariant.load(std::memory_order_relaxed);
-    if (v < 0) {
-        const char *s = std::getenv("MX_BATCH_INVARIANT");
-        int unset = -1;
-        g_invariant.compare_exchange_strong(unset, s && s[0] && s[0] != '0' ? 1 : 0);
-        v = g_invariant.load(std::memory_order_relaxed);
-    }
-    return v == 1;
-}
 // the W8A8 prefill GEMM serves this call (else a GEMV)
 bool use_gemm(int act, int64_t M) {
     return act != ACT_BF16 && M > kGemvMaxM && !batch_invariant();

@@ -184,7 +184,8 @@ static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
 
 // Which form serves a call: 0 streams the weights, 1 and 2 are the tiled form
 // with tiles of up to 128 and 256 rows.  The host knows the rows' number, not
-// their split: the rule goes by the average.  Measured (us, streaming / 128 /
+// their split: the rule goes by the average (in the batch-invariant mode the
+// streaming form serves every call, as K alone fixes its order).  Measured (us, streaming / 128 /
 // 256; e4m3 unless named):
 //   an expert's rows      4            8            16           128
 //   E 32, 4096 x 4096     82/92/92     93/95/95     100/96/96    394/126/114
@@ -202,7 +203,7 @@ static int grouped_form(const GroupedArgs &a) {
         const char *s = std::getenv("MX_GROUPED_FORM");
         return s ? std::atoi(s) : 0;
     }();
-    if (a.E > kGroupedMaxExperts) return 0;
+    if (a.invariant || a.E > kGroupedMaxExperts) return 0;
     if (forced >= 1 && forced <= 3) return forced - 1;
     const int64_t rows = a.M / a.E;                       // an expert's rows, on average
     const int64_t panels = a.E * ((a.N + 255) / 256);

@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(256, 1) grouped_gemm_kernel(GroupedArgs p, int
         }
     }
     __syncthreads();
+    // (offsets that descend could claim more tiles than M rows have: not served)
+    if (upto[0][E - 1] + upto[1][E - 1] > (int)(p.M / 128) + E) return;
     // this XCD's parts of the two lists
     const int xcd = blockIdx.x % 8;
     const int all[2] = {__builtin_amdgcn_readfirstlane(upto[0][E - 1]) * tiles_n,

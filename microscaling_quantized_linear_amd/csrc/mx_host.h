@@ -19,6 +19,8 @@ inline mx_status launched(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ER
 mx_status shape_ok(int elem, int layout, int64_t E, int64_t N, int64_t K);
 // whether the current device is one the kernels are built for
 mx_status device_ok();
+// whether the batch-invariant mode is on (mx_set_batch_invariant)
+bool batch_invariant();
 // one line to stderr with MX_LOG=1
 __attribute__((format(printf, 1, 2))) void log_dispatch(const char *fmt, ...);
 

@@ -197,6 +197,7 @@ struct GroupedArgs {
     uint16_t *y;
     int64_t ldy;
     int epi;                       // 1 = silu(row 2i) * row 2i+1 -> output i (width N / 2)
+    int invariant;                 // 1 = the form whose order of summation K alone fixes
 };
 hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t stream);
 const char *grouped_kernel_name(const GroupedArgs &a);   // for the dispatch trace
@@ -230,9 +231,13 @@ struct LoraArgs {
     uint16_t *y;
     int64_t ldy;
     float *ws;                     // [splits][M][R] partial products x A^T
+    bool invariant;                // the form whose order of summation K alone fixes
 };
 constexpr int64_t kLoraMaxRank = 256;
-int64_t lora_splits(int64_t M, int64_t K);
+constexpr int64_t kLoraMaxCols = 65535 * 256;   // launch-grid rows of 256 columns
+constexpr int64_t kLoraMaxK = int64_t(1) << 26;
+constexpr int64_t kCombineMaxCols = 65535 * 2048;
+int64_t lora_splits(int64_t M, int64_t K, bool invariant);
 hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
 
 }  // namespace mx

@@ -35,28 +35,25 @@ constexpr int expand_waves(int mt) { return mt == 4 ? 8 : 2; }
 
 // Rows of a tile, in units of 16: 64-row tiles read an adapter's matrices a
 // quarter as often, 16-row tiles give four times the workgroups.
-static int lora_mt(int64_t M) { return M >= 512 ? 4 : 1; }
-static int64_t lora_tiles(int64_t M) {
-    const int64_t t = 16 * lora_mt(M);
-    return (M + t - 1) / t;
-}
+static int lora_mt(int64_t M, bool invariant) { return M >= 512 && !invariant ? 4 : 1; }
+static int64_t lora_tiles(int64_t M, int mt) { return (M + 16 * mt - 1) / (16 * mt); }
 // K splits of the shrink.  Few rows: eight units for each of eight wavefronts.
 // Many rows: about a workgroup a compute unit, of at least 1024 values of K:
 // every split's partial sums are read again by all of the expand's column groups.
-int64_t lora_splits(int64_t M, int64_t K) {
-    if (lora_mt(M) == 1) {
+int64_t lora_splits(int64_t M, int64_t K, bool invariant) {
+    if (lora_mt(M, invariant) == 1) {
         const int64_t per = 32 * kUnits * kShrinkWaves;
         return (K + per - 1) / per;
     }
-    const int64_t most = (K + 1023) / 1024, tiles = lora_tiles(M);
+    const int64_t most = (K + 1023) / 1024, tiles = lora_tiles(M, 4);
     const int64_t want = (256 + tiles - 1) / tiles;
     return want < most ? want : most;
 }
 // Workgroups that share a tile's adapters, up to `target` in all: a decode
 // step's rows may all differ, and a tile where two prompts meet would otherwise
 // take twice as long as the rest; those left without an adapter end at once.
-static int lora_shares(int64_t M, int64_t groups, int64_t target) {
-    const int64_t most = 16 * lora_mt(M), want = (target + groups - 1) / groups;
+static int lora_shares(int64_t M, int mt, int64_t groups, int64_t target) {
+    const int64_t most = 16 * mt, want = (target + groups - 1) / groups;
     const int64_t g = want < most ? want : most;
     return (int)(g < M ? g : M);
 }
@@ -69,9 +66,9 @@ __device__ inline int64_t tile_of(const LoraArgs &p, int64_t x) {
     const int64_t t = x % 8 * per + x / 8;
     return t < tiles ? t : -1;
 }
-static int64_t grid_tiles(int64_t M) {
-    const int64_t t = lora_tiles(M);
-    return lora_mt(M) == 4 ? (t + 7) / 8 * 8 : t;
+static int64_t grid_tiles(int64_t M, int mt) {
+    const int64_t t = lora_tiles(M, mt);
+    return mt == 4 ? (t + 7) / 8 * 8 : t;
 }
 
 // Calls f(adapter, mask of its rows) for the tile's distinct adapters number
@@ -502,9 +499,9 @@ __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(Lora
 
 template <int MT, int RT>
 static void shrink(const LoraArgs &a, int splits, hipStream_t st) {
-    const int64_t tiles = lora_tiles(a.M), chunks = (a.R + 16 * RT - 1) / (16 * RT);
-    const int shares = lora_shares(a.M, tiles * splits * chunks, 1024);
-    const dim3 grid((unsigned)grid_tiles(a.M), (unsigned)(splits * chunks), (unsigned)shares);
+    const int64_t tiles = lora_tiles(a.M, MT), chunks = (a.R + 16 * RT - 1) / (16 * RT);
+    const int shares = lora_shares(a.M, MT, tiles * splits * chunks, 1024);
+    const dim3 grid((unsigned)grid_tiles(a.M, MT), (unsigned)(splits * chunks), (unsigned)shares);
     if constexpr (MT == 4)
         hipLaunchKernelGGL(lora_shrink_tiled_kernel<RT>, grid, dim3(256), 0, st, a, splits, shares);
     else
@@ -515,18 +512,18 @@ static void shrink(const LoraArgs &a, int splits, hipStream_t st) {
 template <int MT, int NC, bool STAGED>
 static void expand(const LoraArgs &a, int splits, hipStream_t st) {
     constexpr int waves = expand_waves(MT), cols = 128 * (MT == 4 ? waves / 2 : waves);
-    const int64_t tiles = lora_tiles(a.M), groups = (a.N + cols - 1) / cols;
+    const int64_t tiles = lora_tiles(a.M, MT), groups = (a.N + cols - 1) / cols;
     // the staged form's LDS leaves two places a compute unit: none for idle ones
-    const int shares = lora_shares(a.M, tiles * groups, STAGED ? 512 : 1024);
+    const int shares = lora_shares(a.M, MT, tiles * groups, STAGED ? 512 : 1024);
     const unsigned lds = STAGED ? 0u : (unsigned)(16 * MT * ((a.R + 31) / 32) * 128);
     hipLaunchKernelGGL((lora_expand_kernel<MT, NC, STAGED>),
-                       dim3((unsigned)grid_tiles(a.M), (unsigned)groups, (unsigned)shares),
+                       dim3((unsigned)grid_tiles(a.M, MT), (unsigned)groups, (unsigned)shares),
                        dim3(64 * waves), lds, st, a, splits, shares);
 }
 
 template <int MT>
 static hipError_t launch_mt(const LoraArgs &a, hipStream_t st) {
-    const int splits = (int)lora_splits(a.M, a.K);
+    const int splits = (int)lora_splits(a.M, a.K, a.invariant);
     if (a.R <= 16) shrink<MT, 1>(a, splits, st);
     else if (a.R <= 32) shrink<MT, 2>(a, splits, st);
     else shrink<MT, 4>(a, splits, st);
@@ -539,7 +536,7 @@ static hipError_t launch_mt(const LoraArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_lora(const LoraArgs &a, hipStream_t st) {
-    return lora_mt(a.M) == 4 ? launch_mt<4>(a, st) : launch_mt<1>(a, st);
+    return lora_mt(a.M, a.invariant) == 4 ? launch_mt<4>(a, st) : launch_mt<1>(a, st);
 }
 
 }  // namespace mx

@@ -212,6 +212,7 @@ mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t 
     g.y = static_cast<uint16_t *>(y);
     g.ldy = ldy;
     g.epi = epi;
+    g.invariant = batch_invariant() ? 1 : 0;
     if (act == ACT_MXFP8) {
         uint8_t *data = static_cast<uint8_t *>(ws);
         uint8_t *codes = data + round256(act_t16_data_bytes(M, K));
@@ -250,7 +251,7 @@ mx_status mx_moe_combine(int64_t T, int64_t topk, int64_t N, int64_t M, const vo
                          int64_t ldys, const int32_t *pos, const float *topk_weights, void *y,
                          int64_t ldy, mx_stream_t stream) {
     if (T < 1 || topk < 1 || T > kMaxRows / topk || M < 1 || M > kMaxRows || N < 8 ||
-        N % 8 != 0 || N > kMaxLd ||
+        N % 8 != 0 || N > kCombineMaxCols ||
         ld_bad(ldys, N) || ld_bad(ldy, N))
         return MX_ERR_SHAPE;
     if (!ys || !pos || !topk_weights || !y) return MX_ERR_NULL;
@@ -274,11 +275,12 @@ mx_status mx_moe_combine(int64_t T, int64_t topk, int64_t N, int64_t M, const vo
 mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t M, size_t *bytes) {
     if (!bytes) return MX_ERR_NULL;
     if (L < 1 || L > kMaxRows || R < 8 || R % 8 != 0 || R > kLoraMaxRank || N < 16 ||
-        N % 16 != 0 || K < 32 || K % 32 != 0 || M < 1 || M > kMaxRows)
+        N % 16 != 0 || K < 32 || K % 32 != 0 || M < 1 || M > kMaxRows ||
+        N > kLoraMaxCols || K > kLoraMaxK)
         return MX_ERR_SHAPE;
     // 32-bit offsets into one adapter's matrices
     if (K > kMaxRsrc / (2 * R) || N > kMaxRsrc / (2 * R)) return MX_ERR_SHAPE;
-    *bytes = (size_t)(lora_splits(M, K) * M * ((R + 15) / 16 * 16) * 4);
+    *bytes = (size_t)(lora_splits(M, K, batch_invariant()) * M * ((R + 15) / 16 * 16) * 4);
     return MX_OK;
 }
 
@@ -323,6 +325,7 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
     g.y = static_cast<uint16_t *>(y);
     g.ldy = ldy;
     g.ws = static_cast<float *>(ws);
+    g.invariant = batch_invariant();
     log_dispatch("lora: lora_shrink_kernel, lora_expand_kernel; L=%lld R=%lld M=%lld N=%lld K=%lld",
                  (long long)L, (long long)R, (long long)M, (long long)N, (long long)K);
     return launched(launch_lora(g, hip(stream)));

@@ -33,7 +33,7 @@ hipError_t launch_moe_gather_sum(int64_t, int64_t, int64_t, int64_t, const uint1
 const char *grouped_kernel_name(const GroupedArgs &) { return "grouped"; }
 hipError_t launch_grouped(int, int, const GroupedArgs &, hipStream_t) { return counted(); }
 hipError_t launch_stage_rows(const StageArgs &, int, hipStream_t) { return counted(); }
-int64_t lora_splits(int64_t, int64_t) { return 1; }
+int64_t lora_splits(int64_t, int64_t, bool) { return 1; }
 hipError_t launch_lora(const LoraArgs &, hipStream_t) { return counted(); }
 
 }  // namespace mx

@@ -426,6 +426,63 @@ def test_grouped_many_experts(g, mx):
             check_grouped(y, a, W, offsets, 0)
 
 
+def test_grouped_beyond_the_tile_table(g, mx):
+    """More experts than the tiled form counts (1024): the streaming form serves
+    them, also with many rows."""
+    E, N, K, M = 1100, 32, 64, 9000
+    r = rng(26)
+    w, codes, packed = weight(g, r, 1, 0, E, N, K)
+    W = ref.weights(1, 0, E, N, K, w, codes)
+    x = wl.activations(r, (M, K))
+    a = ref.activations(*oracle.quant_act(x, 0))
+    offsets = split(r, M, E, "skew")
+    y = run_grouped(g, mx, 1, 0, E, N, K, packed, offsets, M, x=x)
+    check_grouped(y, a, W, offsets, 0)
+
+
+def test_grouped_descending_offsets_stay_inside(g, mx):
+    """Offsets that descend: which rows are written is unspecified, but only rows
+    of y are, and the call ends."""
+    import torch
+    r = rng(27)
+    for E, N, K, M in ((4, 64, 256, 40), (200, 64, 256, 3000)):
+        w, codes, packed = weight(g, r, 0, 0, E, N, K)
+        x = wl.activations(r, (M, K))
+        offsets = r.integers(-50, M + 50, E + 1).astype(np.int32)
+        y = out16(g, M + 4, N)
+        need = mx.mx_grouped_workspace(0, 0, E, N, K, M, 1, 0)
+        ws = bytes_(g, need)
+        mx.mx_grouped_linear(0, 0, E, N, K, *packed, M, g.dev(offsets), MXFP8, 0, M, g.dev(x), K,
+                             None, 0, None, 0, None, 0, y, N, ws, need)
+        torch.cuda.synchronize()
+        assert (g.host_u16(y)[M:] == NAN16).all()
+
+
+def test_batch_invariant_mode(g, mx):
+    """With the mode on, a row's grouped product and its adapter's do not depend
+    on the rows beside it: alone, in a small call and in a large one."""
+    r = rng(28)
+    E, N, K, M = 3, 288, 1056, 900
+    w, codes, packed = weight(g, r, 1, 0, E, N, K)
+    x = wl.activations(r, (M, K), 0.01)
+    offsets = np.array([0, 300, 310, 900], np.int32)
+    la, lb, ls, lx, ids, base = lora_inputs(r, 4, 24, N, K, M, "mixed")
+    before = mx.mx_set_batch_invariant(True)
+    try:
+        big = run_grouped(g, mx, 1, 0, E, N, K, packed, offsets, M, x=x)
+        blora = run_lora(g, mx, la, lb, ls, lx, ids, base)
+        for m0, m1 in ((0, 1), (290, 330), (880, 900)):
+            off = np.clip(offsets - m0, 0, m1 - m0)
+            part = run_grouped(g, mx, 1, 0, E, N, K, packed, off, m1 - m0, x=x[m0:m1])
+            assert np.array_equal(part, big[m0:m1])
+            part = run_lora(g, mx, la, lb, ls, lx[m0:m1], ids[m0:m1], base[m0:m1])
+            assert np.array_equal(part, blora[m0:m1])
+    finally:
+        mx.mx_set_batch_invariant(before)
+    W = ref.weights(1, 0, E, N, K, w, codes)
+    check_grouped(big, ref.activations(*oracle.quant_act(x, 0)), W, offsets, 0)
+
+
 # ---- combine ----------------------------------------------------------------------------
 
 

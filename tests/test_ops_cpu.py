@@ -111,7 +111,8 @@ REFUSED = [
     (grouped, WS, [dict(ws=None), dict(wsb=100)]),
     # combine
     (combine, SHAPE, [dict(T=0), dict(topk=0), dict(N=0), dict(N=60), dict(M=0), dict(ldys=56),
-                      dict(ldy=56), dict(T=4000001), dict(T=BIG), dict(ldys=BIG), dict(N=BIG)]),
+                      dict(ldy=56), dict(T=4000001), dict(T=BIG), dict(ldys=BIG), dict(N=BIG),
+                      dict(N=134215688, ldys=134215688, ldy=134215688)]),
     (combine, NULL, [dict(ys=None), dict(pos=None), dict(w=None), dict(y=None)]),
     (combine, ALIGN, [dict(ys=A(0) + 8), dict(ldys=68), dict(pos=A(1) + 2), dict(w=A(2) + 1),
                       dict(y=A(3) + 8), dict(ldy=68)]),
@@ -120,7 +121,8 @@ REFUSED = [
     (lora, SHAPE, [dict(L=0), dict(R=0), dict(R=12), dict(R=264), dict(N=24), dict(N=0),
                    dict(K=48), dict(K=0), dict(M=0), dict(M=4000001), dict(ldx=64), dict(ldb=56),
                    dict(ldy=56), dict(ldx=1 << 28), dict(ldy=1 << 28), dict(K=32 * (1 << 40)),
-                   dict(N=16 * (1 << 40))]),
+                   dict(N=16 * (1 << 40)), dict(R=8, N=16776976, ldb=16776976, ldy=16776976),
+                   dict(R=8, K=(1 << 26) + 32, ldx=(1 << 26) + 32)]),
     (lora, NULL, [dict(a=None), dict(b=None), dict(x=None), dict(ids=None), dict(base=None),
                   dict(y=None)]),
     (lora, ALIGN, [dict(a=A(0) + 8), dict(b=A(1) + 2), dict(x=A(3) + 8), dict(ldx=100),
