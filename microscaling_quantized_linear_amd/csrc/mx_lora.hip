@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 // wavefronts.  K goes in steps of 64 values (128 bytes, a whole line of each
 // row): x and A are copied straight into LDS three steps ahead, eight rows and
 // 1 KB a copy, because operand-shaped loads (64 bytes of 16 rows) reach memory
-// as half lines: x alone then streamed at 2.6 TB/s.  Piece c of a row's
+// as half lines: x alone then streamed at 2.6 TB/s.  x and, in the expand, the
+// projection go past the caches (22 -> 20 and 31 -> 27 us at the sizes below).  Piece c of a row's
 // eight 16-byte pieces stands at c ^ row / 2 % 8, so that the operand reads of 16
 // rows lie in different banks.
 typedef __attribute__((address_space(3))) void lds_void;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(256) lora_shrink_tiled_kernel(LoraArgs p, int 
             for (int i = 0; i < 2; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     xr, (lds_void *)(to + (2 * wave + i) * 1024), 16,
-                    (int)(((xo[i] & ~kOOB) + k) | (xo[i] & kOOB) | past(i)), 0, 0, 0);
+                    (int)(((xo[i] & ~kOOB) + k) | (xo[i] & kOOB) | past(i)), 0, 0, kNT);
 #pragma unroll
             for (int i = 0; i < kA; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(Lora
 #pragma unroll
         for (int i = 0; i < MW; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[i][e] = load16(br, place(i, e, p.ldb, same));
+            for (int e = 0; e < 4; ++e) b[i][e] = load16<kNT>(br, place(i, e, p.ldb, same));
         if constexpr (STAGED) {
             if (!staged) {
                 int id = -1;
