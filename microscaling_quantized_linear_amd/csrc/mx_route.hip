@@ -33,9 +33,12 @@ static int64_t part_pairs(int64_t pairs) {
     return ((pairs + n - 1) / n + unit - 1) / unit * unit;
 }
 
+// a part's histogram: E + 1 counts, padded with zeros to whole 16 bytes
+__host__ __device__ inline int hist_row(int E) { return (E + 4) / 4 * 4; }
+
 int64_t moe_sort_ws_bytes(int64_t E, int64_t pairs) {
     const int64_t n = sort_parts(pairs);
-    return n > 1 ? n * (E + 1) * 4 : 0;
+    return n > 1 ? n * hist_row((int)E) * 4 : 0;
 }
 
 __device__ inline int expert_of(const int32_t *ids, int64_t i, int64_t end, int E) {
@@ -76,10 +79,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(
     const int64_t first = blockIdx.x * part, end = first + part < pairs ? first + part : pairs;
     int kept[kKept];
     count_part(ids, first, end, part / kSortWaves, E, cnt, bins, kept);
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+    for (int b = threadIdx.x; b < hist_row(E); b += kSortThreads) {
         int n = 0;
-        for (int w = 0; w < kSortWaves; ++w) n += cnt[w * bins + b];
-        hist[(int64_t)blockIdx.x * bins + b] = n;
+        for (int w = 0; b < bins && w < kSortWaves; ++w) n += cnt[w * bins + b];
+        hist[(int64_t)blockIdx.x * hist_row(E) + b] = n;
     }
 }
 
@@ -98,22 +101,28 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
     const int64_t per = part / kSortWaves;
     int kept[kKept];
     // total[b]: every part's pairs of expert b; base[b]: those in earlier parts.
-    // Several threads share an expert's parts where the experts are few.
+    // A thread reads four experts' counts at once and, where the experts are few,
+    // several threads share their parts.
     for (int b = threadIdx.x; b < 2 * bins; b += kSortThreads) total[b] = 0;
     count_part(ids, first, end, per, E, cnt, bins, kept);
     if (hist) {
-        const int teams = kSortThreads / bins > 0 ? kSortThreads / bins : 1;
-        for (int i = threadIdx.x; i < teams * bins; i += kSortThreads) {
-            const int b = i % bins, parts = (int)gridDim.x;
-            int before = 0, all = 0;
+        const int quads = hist_row(E) / 4, parts = (int)gridDim.x;
+        const int teams = kSortThreads / quads > 0 ? kSortThreads / quads : 1;
+        for (int i = threadIdx.x; i < teams * quads; i += kSortThreads) {
+            const int b = i % quads * 4;
+            v4i before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
 #pragma unroll 8
-            for (int q = i / bins; q < parts; q += teams) {
-                const int n = hist[(int64_t)q * bins + b];
-                before += q < (int)blockIdx.x ? n : 0;
+            for (int q = i / quads; q < parts; q += teams) {
+                const v4i n = *reinterpret_cast<const v4i *>(hist + (int64_t)q * quads * 4 + b);
+                if (q < (int)blockIdx.x) before += n;
                 all += n;
             }
-            atomicAdd(&total[b], all);
-            atomicAdd(&base[b], before);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (b + k < bins) {
+                    atomicAdd(&total[b + k], all[k]);
+                    atomicAdd(&base[b + k], before[k]);
+                }
         }
         __syncthreads();
     }

@@ -19,7 +19,7 @@ static hipError_t counted() {
 
 hipError_t launch_add_rms_norm(const NormArgs &, int, int, hipStream_t) { return counted(); }
 int64_t moe_sort_ws_bytes(int64_t E, int64_t pairs) {
-    return pairs > 2048 ? (E + 1) * 4 * 2 : 0;
+    return pairs > 2048 ? (E + 4) * 4 * 2 : 0;
 }
 hipError_t launch_moe_sort(int64_t, int64_t, int64_t, const int32_t *, int32_t *, int32_t *,
                            int32_t *, void *, hipStream_t) {
