@@ -16,7 +16,7 @@
 //   expand  v as the sum of two bf16 numbers (its rounding and the rounding's
 //           remainder, 16 significant bits), each with a product of its own
 //           against the same registers of B: v loses nothing that the bf16
-//           result would show, and B is read once.  The residual of the projection is added in
+//           result would show, and B is read once.  The projection is added in
 //           fp32 and y rounded once.
 // Bounds: at decode the adapters' bytes, 2 R (N + K) each, and two launches'
 // latency; at prefill x, base and y, 2 K + 4 N bytes a row.
@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 // row): x and A are copied straight into LDS three steps ahead, eight rows and
 // 1 KB a copy, because operand-shaped loads (64 bytes of 16 rows) reach memory
 // as half lines: x alone then streamed at 2.6 TB/s.  x and, in the expand, the
-// projection go past the caches (22 -> 20 and 31 -> 27 us at the sizes below).  Piece c of a row's
-// eight 16-byte pieces stands at c ^ row / 2 % 8, so that the operand reads of 16
-// rows lie in different banks.
+// projection go past the caches (22 -> 20 and 31 -> 27 us at M = 4096, K = 7168,
+// R = 64, N = 4096).  Piece c of a row's eight 16-byte pieces stands at
+// c ^ row / 2 % 8, so that the operand reads of 16 rows lie in different banks.
 typedef __attribute__((address_space(3))) void lds_void;
 template <int RT>
 __global__ void __launch_bounds__(256) lora_shrink_tiled_kernel(LoraArgs p, int splits,
