@@ -17,7 +17,12 @@
 // four wavefronts split the 128-K steps into contiguous ranges and add their
 // partial tiles in LDS in a fixed order.  Weights stream once from HBM per
 // batch; activations come from L2.  An expert without rows costs one load of
-// its offsets.
+// its offsets.  NT = 2 for e4m3 and 4 for e2m1 keep as many bytes in flight and
+// enough workgroups (E 32, 4096 x 4096, 4 rows an expert: e4m3 82 us, with NT 1
+// 93 and 4 98; e2m1 44 us, 6.1 TB/s, with NT 2 52 and 8 64; eight wavefronts 102
+// and 59, two 82 and 47).  The weights go past the caches where a batch mostly
+// takes all of an expert's rows (82 us, with caches 89); batches of 64 rows read
+// them again, from the caches (E 16, 2048 x 7168, 48 rows: 82 -> 61 us).
 #include "mx_device.h"
 #include "mx_kernels.h"
 
@@ -44,6 +49,7 @@ struct StreamStep {
 
 template <int ELEM, int LAYOUT, int MT, int NT>
 __global__ void __launch_bounds__(64 * kStreamWaves) grouped_stream_kernel(GroupedArgs p) {
+    constexpr int kAux = MT == 4 ? 0 : kNT;
     __shared__ v4f red[kStreamWaves][NT * MT][64];
     const int64_t e = blockIdx.y;
     // ranges that break the rules are cut to [0, M)
@@ -92,9 +98,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves) grouped_stream_kernel(Group
                 const uint32_t o = 16u * lane;
                 const uint32_t base = (uint32_t)(t * TILEB + (int64_t)s * CHUNK) & ~kOOB;
                 const bool last = s == S - 1;
-                st.w0[t] = load16<kNT>(wr, (base + o) | past | (last && o >= tailb ? kOOB : 0u));
+                st.w0[t] = load16<kAux>(wr, (base + o) | past | (last && o >= tailb ? kOOB : 0u));
                 if (ELEM == E4M3)
-                    st.w1[t] = load16<kNT>(
+                    st.w1[t] = load16<kAux>(
                         wr, (base + 1024u + o) | past | (last && o + 1024u >= tailb ? kOOB : 0u));
                 st.cw[t] = load4(cr, (LAYOUT == ROW32
                                           ? (uint32_t)(t * Q + s / 4) * 256u + 4u * lane
@@ -168,9 +174,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves) grouped_stream_kernel(Group
     }
 }
 
-template <int ELEM, int LAYOUT>
+template <int ELEM, int LAYOUT, int NT>
 static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
-    constexpr int NT = 2;
     const dim3 grid((unsigned)((a.N / 16 + NT - 1) / NT), (unsigned)a.E), block(64 * kStreamWaves);
     const int64_t rows = a.M / a.E;                       // an expert's rows, on average
     if (rows <= 6)
@@ -188,15 +193,15 @@ static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
 // streaming form serves every call, as K alone fixes its order).  Measured (us, streaming / 128 /
 // 256; e4m3 unless named):
 //   an expert's rows      4            8            16           128
-//   E 32, 4096 x 4096     82/92/92     93/95/95     100/96/96    394/126/114
-//   the same, e2m1        51/52/53     62/55/55     66/55/56     273/87/81
-//   E 24, 4096 x 1568     24/30/30                  43/31/31
-//   E 64, 512 x 2048      14/17/17                  23/18/18     89/22/28
+//   E 32, 4096 x 4096     83/92/92     94/95/95     100/95/95    352/126/115
+//   the same, e2m1        44/50/50     55/55/54     57/56/56     218/92/82
+//   E 24, 4096 x 1568     29/31/31     37/31        41/32/32
+//   E 64, 512 x 2048      14/17/17                  23/18/18     75/21/28
 // and with fewer weight panels (of 256 rows) than half the compute units, where
 // the tiled form leaves the others idle:
-//   an expert's rows      64           128          256          1024       4096
-//   E 1, 4096 x 4096      10/23/23     20/23/23     36/24/39     142/28/42  557/66/59
-//   E 8, 1024 x 1024      6/10/10      9/11/11                   (512: 33/13/18)
+//   an expert's rows      64           128          192       256        1024
+//   E 1, 4096 x 4096      9/23/23      16/23/24     22/24     29/24/39   108/27/42
+//   E 8, 1024 x 1024      7/10/10      8/11/11      12/12                (512: 29/13/18)
 // MX_GROUPED_FORM (1 to 3) overrides the rule (tuning sweeps only; read once).
 static int grouped_form(const GroupedArgs &a) {
     static const int forced = [] {
@@ -207,7 +212,7 @@ static int grouped_form(const GroupedArgs &a) {
     if (forced >= 1 && forced <= 3) return forced - 1;
     const int64_t rows = a.M / a.E;                       // an expert's rows, on average
     const int64_t panels = a.E * ((a.N + 255) / 256);
-    if (rows <= (panels < 128 ? 128 : 6)) return 0;
+    if (rows <= (panels < 128 ? 192 : 6)) return 0;
     return rows >= 128 && panels * ((rows + 255) / 256) >= 256 ? 2 : 1;
 }
 
@@ -221,8 +226,12 @@ const char *grouped_kernel_name(const GroupedArgs &a) {
 hipError_t launch_grouped(int elem, int layout, const GroupedArgs &a, hipStream_t st) {
     if (const int form = grouped_form(a))
         return launch_grouped_gemm(elem, layout, 128 * form, a, st);
-    if (elem == E2M1) return launch_stream<E2M1, ROW32>(a, st);
-    return layout == ROW32 ? launch_stream<E4M3, ROW32>(a, st) : launch_stream<E4M3, BLK32>(a, st);
+    // (e2m1: four tiles a workgroup while that leaves two workgroups a compute unit)
+    if (elem == E2M1)
+        return a.E * (a.N / 64) >= 512 ? launch_stream<E2M1, ROW32, 4>(a, st)
+                                       : launch_stream<E2M1, ROW32, 2>(a, st);
+    return layout == ROW32 ? launch_stream<E4M3, ROW32, 2>(a, st)
+                           : launch_stream<E4M3, BLK32, 2>(a, st);
 }
 
 // ---- staging: the grouped rows' activation in the T16 layout ----
