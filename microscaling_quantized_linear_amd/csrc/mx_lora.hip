@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(Lora
             const int row = n / (chunks * 8), rank = n % (chunks * 8) * 4;
             v4f s = {0.f, 0.f, 0.f, 0.f};
             float scale = 1.0f;
-            if ((rows >> row & 1) && rank < Rp) {
+            // (ranks from R on: zeros, not the products of A's missing rows, which an
+            // infinite x turns into NaN)
+            if ((rows >> row & 1) && rank < p.R) {
                 if (p.scales) scale = p.scales[p.ids[m0 + row]];
                 const float *at = p.ws + (m0 + row) * Rp + rank;
 #pragma unroll 4
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(Lora
             for (int i = 0; i < 4; ++i) {
                 const float v = s[i] * scale;
                 hi[i] = bf16_bits(v);
-                lo[i] = bf16_bits(v - bf16_to_f32(hi[i]));
+                // (an infinity has no remainder: inf - inf would be NaN)
+                lo[i] = (hi[i] & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(v - bf16_to_f32(hi[i]));
             }
             uint16_t *to = vs + ((rank / 32) * 32 * MT + row) * 32 +
                            8 * ((rank % 32 / 8) ^ (row / 4 % 4)) + rank % 8;

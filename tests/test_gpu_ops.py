@@ -578,6 +578,22 @@ def test_lora_rows_without_adapter_are_not_read(g, mx):
         ref.assert_within(y, out, tol, "lora")
 
 
+@pytest.mark.parametrize("R", [8, 24, 40, 72])
+@pytest.mark.parametrize("M", [20, 600])
+def test_lora_infinite_inputs(g, mx, M, R):
+    """With positive A and B an infinite x makes its row infinite (not NaN), and
+    leaves the other rows alone."""
+    a, b, s, x, ids, base = lora_inputs(rng(42, M, R), 5, R, 96, 160, M, "each")
+    a, b = a & 0x7FFF | 0x0080, b & 0x7FFF | 0x0080       # positive, none zero
+    out, tol = ref.lora(x, a, b, s, ids, base)
+    up, down = np.arange(1, M, 7), np.arange(3, M, 7)
+    x[up, up % 160], x[down, down % 160] = 0x7F80, 0xFF80
+    rest = np.setdiff1d(np.arange(M), np.concatenate([up, down]))
+    y = run_lora(g, mx, a, b, s, x, ids, base)
+    assert (y[up] == 0x7F80).all() and (y[down] == 0xFF80).all()
+    ref.assert_within(y[rest], out[rest], tol[rest], "lora")
+
+
 # ---- together, other streams, graphs, long buffers ---------------------------------------------
 
 
