@@ -186,7 +186,11 @@ mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t 
         if (!aligned16(ws)) return MX_ERR_ALIGN;
     }
     const Span sy{y, M, ldy, width, 2};
+    size_t wb = 0, cb = 0;
+    if ((st = mx_packed_sizes(elem, layout, E, N, K, &wb, &cb)) != MX_OK) return st;
     const Span ins[] = {
+        {w_packed, 1, 0, (int64_t)wb, 1},
+        {codes_packed, 1, 0, (int64_t)cb, 1},
         {act == ACT_MXFP8 && !given ? x : nullptr, xrows, ldx, K, 2},
         {act == ACT_MXFP8 && given ? xq : nullptr, xrows, ldq, K, 1},
         {act == ACT_MXFP8 && given ? xcodes : nullptr, xrows, ldc, K / 32, 1},

@@ -158,6 +158,26 @@ def test_refusals(call, status, cases):
         assert call(**kw) == status, kw
 
 
+def test_grouped_outputs_on_the_weights_are_refused():
+    """y or the workspace anywhere in the packed weights or codes."""
+    for elem, layout in ((0, 0), (0, 1), (1, 0)):
+        wb, cb = mx.mx_packed_sizes(elem, layout, 4, 64, 256)
+        last_w, last_c = (wb - 1) // 16 * 16, (cb - 1) // 16 * 16
+        for kw in (dict(y=A(0)), dict(y=A(0) + last_w), dict(y=A(1)), dict(y=A(1) + last_c),
+                   dict(y=A(0) - 2048), dict(ws=A(0) + 256), dict(ws=A(1) + last_c)):
+            assert grouped(elem=elem, layout=layout, **kw) == UNSUP, (elem, layout, kw)
+
+
+def test_grouped_outputs_behind_the_weights_are_in_order():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the fake addresses must not reach a GPU")
+    for elem, layout in ((0, 0), (0, 1), (1, 0)):
+        wb, cb = mx.mx_packed_sizes(elem, layout, 4, 64, 256)
+        for kw in (dict(y=A(0) + (wb + 15) // 16 * 16), dict(ws=A(1) + (cb + 15) // 16 * 16)):
+            assert grouped(elem=elem, layout=layout, **kw) == DEVICE, (elem, layout, kw)
+
+
 def test_valid_calls_reach_the_device_gate():
     import torch
     if torch.cuda.is_available():
