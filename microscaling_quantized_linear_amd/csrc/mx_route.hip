@@ -161,7 +161,12 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
     }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < bins; b += kSortThreads) offsets[b] = total[b];
-    // the pairs, 64 of a wavefront at a time and in order
+    // the pairs, 64 of a wavefront at a time and in order.  LDS operations of a
+    // wavefront complete in order; the compiler is told to keep them so.
+    auto wave_order = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+    };
     int *mine = cnt + wave * bins;
     auto put = [&](int e, int64_t pair) {
         uint64_t same = __ballot(e >= 0);
@@ -172,16 +177,15 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(
         if (e >= 0) {
             const int rank = __popcll(same & ((1ull << lane) - 1ull));
             const int at = mine[e] + rank;
-            __builtin_amdgcn_wave_barrier();
             const int place = total[e] + at;
             rows[place] = e < E ? (int32_t)((uint32_t)pair / (uint32_t)topk) : -1;
             pos[pair] = e < E ? place : -1;
             // the last lane of the expert moves its count on, once every lane
-            // of the wavefront has read it (LDS operations of a wavefront
-            // complete in order)
+            // of the wavefront has read it
+            wave_order();
             if (rank == __popcll(same) - 1) mine[e] = at + 1;
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_order();
     };
     const int64_t at = first + wave * per + lane;
 #pragma unroll
