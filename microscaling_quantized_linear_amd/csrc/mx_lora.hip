@@ -91,14 +91,14 @@ __device__ inline uint64_t each_adapter(const LoraArgs &p, int64_t m0, int rows,
     return all;
 }
 
-// Few rows (one 16-row tile, MT = 1): operands straight from memory.
-template <int MT, int RT>
+// Few rows (one 16-row tile): operands straight from memory.
+template <int RT>
 __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs p, int splits,
                                                                         int shares) {
-    __shared__ v4f red[kShrinkWaves][MT][64];
+    __shared__ v4f red[kShrinkWaves][64];
     const int lane = threadIdx.x % 64, r = lane % 16, j = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * MT);
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
     const int split = blockIdx.y % splits, rank0 = blockIdx.y / splits * (16 * RT);
     const int share = blockIdx.z;
     const int64_t Rp = (p.R + 15) / 16 * 16;
@@ -107,34 +107,30 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
     const int part = split * kShrinkWaves + wave;
     const int u0 = (int)((int64_t)units * part / parts);
     const int u1 = (int)((int64_t)units * (part + 1) / parts);
-    const int64_t left = p.M - m0 < 16 * MT ? p.M - m0 : 16 * MT;
+    const int64_t left = p.M - m0 < 16 ? p.M - m0 : 16;
     const __amdgpu_buffer_rsrc_t xr =
         make_rsrc(p.x + m0 * p.ldx, (uint32_t)(((left - 1) * p.ldx + p.K) * 2));
     const uint32_t row_bytes = (uint32_t)(p.K * 2);
 
-    each_adapter(p, m0, 16 * MT, share, shares, [&](int g, uint64_t same) {
+    each_adapter(p, m0, 16, share, shares, [&](int g, uint64_t same) {
         const __amdgpu_buffer_rsrc_t ar =
             make_rsrc(p.a + (int64_t)g * p.R * p.K, (uint32_t)(p.R * p.K * 2));
-        uint32_t xo[MT], ao[RT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            xo[t] = same >> (16 * t + r) & 1 ? (uint32_t)((16 * t + r) * p.ldx * 2) : kOOB;
+        const uint32_t xo = same >> r & 1 ? (uint32_t)(r * p.ldx * 2) : kOOB;
+        uint32_t ao[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const int rank = rank0 + 16 * t + r;
             ao[t] = rank < p.R ? (uint32_t)rank * row_bytes : kOOB;
         }
-        v4f acc[RT][MT];
+        v4f acc[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) acc[t][i] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
         // P units a batch, in straight line so that each batch's loads are out
         // ahead of the products of the one before; a unit past the wavefront's
         // range reads zeros
-        constexpr int P = RT * MT >= 8 ? 2 : RT * MT >= 4 ? 4 : 8;
+        constexpr int P = RT >= 4 ? 4 : 8;
         constexpr int NB = kUnits / P;
-        v4u av[2][P][RT], xv[2][P][MT];
+        v4u av[2][P][RT], xv[2][P];
         auto load = [&](int n, int u) {
 #pragma unroll
             for (int q = 0; q < P; ++q) {
@@ -143,9 +139,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
                     av[n][q][t] = load16(ar, ((ao[t] & ~kOOB) + k) | (ao[t] & kOOB) | past);
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    xv[n][q][t] = load16(xr, ((xo[t] & ~kOOB) + k) | (xo[t] & kOOB) | past);
+                xv[n][q] = load16(xr, ((xo & ~kOOB) + k) | (xo & kOOB) | past);
             }
         };
         load(0, u0);
@@ -157,27 +151,23 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
             for (int q = 0; q < P; ++q)
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        acc[t][i] = mfma_bf16(as_bf16x8(av[n % 2][q][t]),
-                                              as_bf16x8(xv[n % 2][q][i]), acc[t][i]);
+                    acc[t] = mfma_bf16(as_bf16x8(av[n % 2][q][t]), as_bf16x8(xv[n % 2][q]),
+                                       acc[t]);
             __builtin_amdgcn_sched_barrier(0);
         }
         // element i of lane (j, r): rank 4 j + i, token r of each 16 x 16 tile
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[t][i];
+            red[wave][lane] = acc[t];
             __syncthreads();
-            for (int n = threadIdx.x; n < MT * 64; n += 64 * kShrinkWaves) {
-                const int i = n / 64, l = n % 64;
-                v4f s = red[0][i][l];
+            if (wave == 0) {
+                v4f s = red[0][lane];
 #pragma unroll
-                for (int w = 1; w < kShrinkWaves; ++w) s += red[w][i][l];
-                const int row = 16 * i + l % 16, rank = rank0 + 16 * t + 4 * (l / 16);
-                if ((same >> row & 1) && rank < Rp)
-                    *reinterpret_cast<v4f *>(p.ws + ((int64_t)split * p.M + m0 + row) * Rp +
-                                             rank) = s;
+                for (int w = 1; w < kShrinkWaves; ++w) s += red[w][lane];
+                const int rank = rank0 + 16 * t + 4 * j;
+                if ((same >> r & 1) && rank < Rp)
+                    *reinterpret_cast<v4f *>(p.ws + ((int64_t)split * p.M + m0 + r) * Rp + rank) =
+                        s;
             }
             __syncthreads();
         }
@@ -509,8 +499,8 @@ static void shrink(const LoraArgs &a, int splits, hipStream_t st) {
     if constexpr (MT == 4)
         hipLaunchKernelGGL(lora_shrink_tiled_kernel<RT>, grid, dim3(256), 0, st, a, splits, shares);
     else
-        hipLaunchKernelGGL((lora_shrink_kernel<MT, RT>), grid, dim3(64 * kShrinkWaves), 0, st, a,
-                           splits, shares);
+        hipLaunchKernelGGL(lora_shrink_kernel<RT>, grid, dim3(64 * kShrinkWaves), 0, st, a, splits,
+                           shares);
 }
 
 template <int MT, int NC, bool STAGED>

@@ -11,8 +11,8 @@
 // without a change in its results.
 //
 // Work split: a row is cut into segments of 512 values, eight a lane (one
-// 16-byte load of x and one of the residual).  W wavefronts share a row,
-// wavefront w taking segments w, w + W, ...; the row stays in registers
+// 16-byte load of x and one of the residual).  Eight wavefronts share a row,
+// wavefront w taking segments w, w + 8, ...; the row stays in registers
 // between the sum of squares and the output, so x and the residual are read
 // once.  A quad of lanes holds one 32-value block, so the block maximum is two
 // DPP steps, and a segment is exactly one quad of 128-K steps of the T16
@@ -20,9 +20,9 @@
 // x, the residual and the stored sum go past the caches (the sum is next read a
 // layer later): M = 4096, K = 7168 with every output, 265 MB, 48.5 -> 42.5 us,
 // 6.2 TB/s; y and the bytes, which the next product reads, do not.
-// The order of the sum of squares does not depend on W: segments c, c + 8, ...
-// are one of eight partial sums of a lane, the eight are added as a tree, then
-// the 64 lanes.  A row's result is therefore the same in any call.
+// The order of the sum of squares is fixed by K: a lane's values, the eight
+// wavefronts as a tree, then the 64 lanes.  A row's result is therefore the same
+// in any call.
 #include "mx_device.h"
 #include "mx_kernels.h"
 
@@ -35,14 +35,14 @@ __device__ inline void store16(__amdgpu_buffer_rsrc_t r, v4u v, uint32_t off) {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, AUX);
 }
 
-// W wavefronts a row, at most NS segments a wavefront; ACT as in mx_act
-template <int W, int NS, int ACT, int RULE>
-__global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
-    constexpr int R = 8 / W;                              // rows per workgroup
+constexpr int kRowWaves = 8;               // wavefronts, and one row a workgroup
+
+// at most NS segments a wavefront; ACT as in mx_act
+template <int NS, int ACT, int RULE>
+__global__ void __launch_bounds__(64 * kRowWaves) add_rms_norm_kernel(NormArgs p) {
     const int lane = threadIdx.x % 64;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t m = (int64_t)blockIdx.x * R + wave / W;
-    const int w = wave % W;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t m = blockIdx.x;
     const int K = (int)p.K;
     const bool live = m < p.M;                            // T16: rows past M pad the last tile
     const uint32_t rowb = live ? (uint32_t)K * 2u : 0u;
@@ -57,24 +57,20 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
     v4u v[NS], wt[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        v[i] = load16<kNT>(xr, (uint32_t)(1024 * (w + W * i) + 16 * lane));
+        v[i] = load16<kNT>(xr, (uint32_t)(1024 * (w + kRowWaves * i) + 16 * lane));
     v4u res[NS];
     if (p.res) {
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            res[i] = load16<kNT>(rr, (uint32_t)(1024 * (w + W * i) + 16 * lane));
+            res[i] = load16<kNT>(rr, (uint32_t)(1024 * (w + kRowWaves * i) + 16 * lane));
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) wt[i] = load16(wr, (uint32_t)(1024 * (w + W * i) + 16 * lane));
+    for (int i = 0; i < NS; ++i)
+        wt[i] = load16(wr, (uint32_t)(1024 * (w + kRowWaves * i) + 16 * lane));
 
-    // the segment's class c % 8 is one partial sum (W == 8: the wavefront's own)
-    constexpr int NC = 8 / W;
-    float part[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) part[c] = 0.0f;
+    float acc = 0.0f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        float &acc = part[i % NC];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             uint32_t u = v[i][d];
@@ -89,22 +85,15 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
             acc = __builtin_fmaf(lo, lo, acc);
             acc = __builtin_fmaf(hi, hi, acc);
         }
-        if (p.sum) store16<kNT>(sr, v[i], (uint32_t)(1024 * (w + W * i) + 16 * lane));
+        if (p.sum) store16<kNT>(sr, v[i], (uint32_t)(1024 * (w + kRowWaves * i) + 16 * lane));
     }
-    float ss;
-    if constexpr (W == 8) {
-        __shared__ float red[8][64];
-        red[w][lane] = part[0];
-        __syncthreads();
-        float t[8];
+    __shared__ float red[kRowWaves][64];
+    red[w][lane] = acc;
+    __syncthreads();
+    float t[kRowWaves];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) t[c] = red[c][lane];
-        ss = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-    } else {
-        static_assert(W == 1, "one wavefront a row, or all eight");
-        ss = ((part[0] + part[1]) + (part[2] + part[3])) +
-             ((part[4] + part[5]) + (part[6] + part[7]));
-    }
+    for (int c = 0; c < kRowWaves; ++c) t[c] = red[c][lane];
+    float ss = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) ss += __shfl_xor(ss, o);
     const float scale = 1.0f / __builtin_sqrtf(ss / (float)K + p.eps);
@@ -130,7 +119,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
     const __amdgpu_buffer_rsrc_t qr = make_rsrc(qbase, qbytes);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        const int c = w + W * i;                          // segment
+        const int c = w + kRowWaves * i;                          // segment
         const int k0 = 512 * c + 8 * lane;
         v4u o;
 #pragma unroll
@@ -162,31 +151,32 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(NormArgs p) {
     }
 }
 
-template <int W, int NS, int ACT>
+template <int NS, int ACT>
 static hipError_t launch_rule(const NormArgs &a, int64_t rows, int rule, hipStream_t st) {
-    const dim3 grid((unsigned)((rows * W + 7) / 8)), block(512);
+    const dim3 grid((unsigned)rows), block(64 * kRowWaves);
     if (rule == RULE_OCP)
-        hipLaunchKernelGGL((add_rms_norm_kernel<W, NS, ACT, RULE_OCP>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((add_rms_norm_kernel<NS, ACT, RULE_OCP>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((add_rms_norm_kernel<W, NS, ACT, RULE_CEIL448>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((add_rms_norm_kernel<NS, ACT, RULE_CEIL448>), grid, block, 0, st, a);
     return hipGetLastError();
 }
 
-template <int W, int NS>
+template <int NS>
 static hipError_t launch_act(const NormArgs &a, int64_t rows, int act, int rule, hipStream_t st) {
-    if (act == ACT_BF16) return launch_rule<W, NS, ACT_BF16>(a, rows, RULE_OCP, st);
-    if (act == ACT_MXFP8) return launch_rule<W, NS, ACT_MXFP8>(a, rows, rule, st);
-    return launch_rule<W, NS, ACT_MXFP8_T16>(a, rows, rule, st);
+    // (a bf16 output does not depend on the rule)
+    if (act == ACT_BF16) return launch_rule<NS, ACT_BF16>(a, rows, RULE_OCP, st);
+    if (act == ACT_MXFP8) return launch_rule<NS, ACT_MXFP8>(a, rows, rule, st);
+    return launch_rule<NS, ACT_MXFP8_T16>(a, rows, rule, st);
 }
 
 hipError_t launch_add_rms_norm(const NormArgs &a, int act, int rule, hipStream_t st) {
     const int64_t segs = (a.K + 511) / 512;
     const int64_t rows = act == ACT_MXFP8_T16 ? (a.M + 15) / 16 * 16 : a.M;
-    if (segs <= 8) return launch_act<8, 1>(a, rows, act, rule, st);
-    if (segs <= 16) return launch_act<8, 2>(a, rows, act, rule, st);
-    if (segs <= 32) return launch_act<8, 4>(a, rows, act, rule, st);
-    if (segs <= 64) return launch_act<8, 8>(a, rows, act, rule, st);
-    return launch_act<8, 16>(a, rows, act, rule, st);
+    if (segs <= 8) return launch_act<1>(a, rows, act, rule, st);
+    if (segs <= 16) return launch_act<2>(a, rows, act, rule, st);
+    if (segs <= 32) return launch_act<4>(a, rows, act, rule, st);
+    if (segs <= 64) return launch_act<8>(a, rows, act, rule, st);
+    return launch_act<16>(a, rows, act, rule, st);
 }
 
 }  // namespace mx
