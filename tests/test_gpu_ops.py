@@ -440,6 +440,22 @@ def test_grouped_beyond_the_tile_table(g, mx):
     check_grouped(y, a, W, offsets, 0)
 
 
+@pytest.mark.parametrize("E,N,K,M", [
+    (512, 96, 544, 1500), (270, 160, 288, 700), (1030, 96, 96, 12000), (1030, 96, 160, 25000)])
+def test_grouped_panels_cut_short(g, mx, E, N, K, M):
+    """Many experts: the streaming form's panels of four weight tiles, the last
+    of an expert with fewer, at each of its batch sizes."""
+    r = rng(27, E, M)
+    w, codes, packed = weight(g, r, 1, 0, E, N, K)
+    W = ref.weights(1, 0, E, N, K, w, codes)
+    x = wl.activations(r, (M, K))
+    a = ref.activations(*oracle.quant_act(x, 0))
+    offsets = split(r, M, E, "skew")
+    for epi in (0, 1):
+        y = run_grouped(g, mx, 1, 0, E, N, K, packed, offsets, M, x=x, epi=epi)
+        check_grouped(y, a, W, offsets, epi)
+
+
 def test_grouped_descending_offsets_stay_inside(g, mx):
     """Offsets that descend: which rows are written is unspecified, but only rows
     of y are, and the call ends."""
