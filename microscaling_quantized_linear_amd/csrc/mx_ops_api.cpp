@@ -276,16 +276,22 @@ mx_status mx_moe_combine(int64_t T, int64_t topk, int64_t N, int64_t M, const vo
                                           hip(stream)));
 }
 
-mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t M, size_t *bytes) {
-    if (!bytes) return MX_ERR_NULL;
+// the adapters' workspace in a given batch-invariant mode
+static mx_status lora_bytes(int64_t L, int64_t R, int64_t N, int64_t K, int64_t M, bool invariant,
+                            size_t *bytes) {
     if (L < 1 || L > kMaxRows || R < 8 || R % 8 != 0 || R > kLoraMaxRank || N < 16 ||
         N % 16 != 0 || K < 32 || K % 32 != 0 || M < 1 || M > kMaxRows ||
         N > kLoraMaxCols || K > kLoraMaxK)
         return MX_ERR_SHAPE;
     // 32-bit offsets into one adapter's matrices
     if (K > kMaxRsrc / (2 * R) || N > kMaxRsrc / (2 * R)) return MX_ERR_SHAPE;
-    *bytes = (size_t)(lora_splits(M, K, batch_invariant()) * M * ((R + 15) / 16 * 16) * 4);
+    *bytes = (size_t)(lora_splits(M, K, invariant) * M * ((R + 15) / 16 * 16) * 4);
     return MX_OK;
+}
+
+mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t M, size_t *bytes) {
+    if (!bytes) return MX_ERR_NULL;
+    return lora_bytes(L, R, N, K, M, batch_invariant(), bytes);
 }
 
 mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a, const void *b,
@@ -293,7 +299,10 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
                       const int32_t *ids, const void *base, int64_t ldb, void *y, int64_t ldy,
                       void *ws, size_t ws_bytes, mx_stream_t stream) {
     size_t need = 0;
-    mx_status st = mx_lora_workspace(L, R, N, K, M, &need);
+    // read once: the launch writes what the size checked here has room for, also
+    // when another thread changes the mode meanwhile
+    const bool invariant = batch_invariant();
+    mx_status st = lora_bytes(L, R, N, K, M, invariant, &need);
     if (st != MX_OK) return st;
     if (ldx < K || ldb < N || ldy < N) return MX_ERR_SHAPE;
     // 32-bit offsets into a tile of 64 rows
@@ -329,7 +338,7 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
     g.y = static_cast<uint16_t *>(y);
     g.ldy = ldy;
     g.ws = static_cast<float *>(ws);
-    g.invariant = batch_invariant();
+    g.invariant = invariant;
     log_dispatch("lora: lora_shrink_kernel, lora_expand_kernel; L=%lld R=%lld M=%lld N=%lld K=%lld",
                  (long long)L, (long long)R, (long long)M, (long long)N, (long long)K);
     return launched(launch_lora(g, hip(stream)));

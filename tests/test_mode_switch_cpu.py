@@ -1,0 +1,66 @@
+"""A call reads the batch-invariant mode once: another thread that changes the
+mode between the check of the workspace and the launch (played by stand-ins
+that change it at exactly that point) cannot make the launch write more than
+the checked size.  On a host-only build of the library's host code."""
+import ctypes as C
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+import microscaling_quantized_linear_amd as mx  # noqa: E402
+
+
+def A(i):
+    """Fake, distinct, 256-byte aligned device addresses: never dereferenced."""
+    return (i + 1) << 40
+
+
+@pytest.fixture(scope="module")
+def host_lib(tmp_path_factory):
+    csrc = os.path.join(ROOT, "microscaling_quantized_linear_amd", "csrc")
+    lib = str(tmp_path_factory.mktemp("mode") / "libmx_mode.so")
+    src = [os.path.join(csrc, f) for f in ("mx_api.cpp", "mx_ops_api.cpp")]
+    src += [os.path.join(ROOT, "tests", "sanitize", f)
+            for f in ("host_stubs.cpp", "mode_stubs.cpp")]
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+                        "-I/opt/rocm/include", *src, "-o", lib], capture_output=True, text=True)
+    if r.returncode != 0 and "hip_runtime.h" in r.stderr:
+        pytest.skip("HIP headers not found")
+    assert r.returncode == 0, r.stderr[-3000:]
+    return lib
+
+
+def child(lib, what):
+    r = subprocess.run([sys.executable, os.path.abspath(__file__), lib, what], capture_output=True,
+                       text=True, env=dict(os.environ, MX_LOG="1"), timeout=300)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+    assert f"{what} ok" in r.stdout
+    return r.stderr
+
+
+def test_adapters(host_lib):
+    child(host_lib, "adapters")
+
+
+def _adapters(L):
+    switch, written = C.c_int.in_dll(L, "mx_switch_to"), C.c_long.in_dll(L, "mx_lora_written")
+    need, M = C.c_size_t(), 4096
+    for before, after in ((1, 0), (0, 1)):
+        switch.value = -1
+        L.mx_set_batch_invariant(before)
+        assert L.mx_lora_workspace(8, 64, 4096, 7168, M, C.byref(need)) == 0
+        switch.value = after
+        status = L.mx_lora_add(8, 64, 4096, 7168, A(0), A(1), None, M, A(2), 7168, A(3), A(4),
+                               4096, A(5), 4096, A(6), need.value, None)
+        assert status == 0 and written.value == need.value, (before, status, written.value)
+
+
+if __name__ == "__main__":
+    mx.LIB_PATH = sys.argv[1]
+    {"adapters": _adapters}[sys.argv[2]](mx.lib())
+    print(sys.argv[2], "ok")
