@@ -108,7 +108,8 @@ using mx::ROW32;
 // largest M served by the decode GEMV for W8A8; above it the GEMM runs
 constexpr int64_t kGemvMaxM = 64;
 
-// the W8A8 prefill GEMM serves this call (else a GEMV)
+// the W8A8 prefill GEMM serves this call (else a GEMV); reads the batch-invariant
+// mode, so a call asks once and keeps the answer
 bool use_gemm(int act, int64_t M) {
     return act != ACT_BF16 && M > kGemvMaxM && !batch_invariant();
 }
@@ -137,6 +138,21 @@ bool fused_quant_ok(int elem, int64_t N, int64_t K, int64_t M) {
     }();
     return enabled && elem == E4M3 && M <= kGemvMaxM && K % 128 == 0 &&
            mx::gemv_w8_even(N, K, gemv_w8_plan(N, K, M));
+}
+
+// mx_linear's workspace for valid arguments, by whether the GEMM serves the call
+size_t linear_bytes(int elem, int64_t N, int64_t K, int64_t M, int act, bool prequantized,
+                    bool gemm) {
+    const bool long_k = !gemm && !gemv_w8_plan(N, K, M).ok;
+    if (act == ACT_MXFP8 && !prequantized && fused_quant_ok(elem, N, K, M))
+        return 0;                                       // quantized inside the GEMV
+    if (act == ACT_MXFP8 && !prequantized && !long_k)   // in-call quantization into T16
+        return (size_t)(round256(mx::act_t16_data_bytes(M, K)) + mx::act_codes_t16_bytes(M, K));
+    if (act == ACT_MXFP8 && !prequantized)              // row-major, chunked GEMV for long K
+        return (size_t)(round256(M * padded_k(K)) + round256(M * (padded_k(K) / 32)));
+    if (act == ACT_MXFP8 && gemm)                       // row-major input restaged into T16
+        return (size_t)(round256(mx::act_t16_data_bytes(M, K)) + mx::act_codes_t16_bytes(M, K));
+    return 0;
 }
 
 const char *layout_name(int layout) { return layout == ROW32 ? "ROW32" : "BLK32"; }
@@ -370,17 +386,7 @@ mx_status mx_linear_workspace(int elem, int layout, int64_t N, int64_t K, int64_
     if (st != MX_OK) return st;
     if (M < 1) return MX_ERR_SHAPE;
     if (act != ACT_BF16 && act != ACT_MXFP8 && act != ACT_MXFP8_T16) return MX_ERR_UNSUPPORTED;
-    *bytes = 0;
-    const bool gemm = use_gemm(act, M);
-    const bool long_k = !gemm && !gemv_w8_plan(N, K, M).ok;
-    if (act == ACT_MXFP8 && !prequantized && fused_quant_ok(elem, N, K, M))
-        return MX_OK;                                   // quantized inside the GEMV
-    if (act == ACT_MXFP8 && !prequantized && !long_k)   // in-call quantization into T16
-        *bytes = (size_t)(round256(mx::act_t16_data_bytes(M, K)) + mx::act_codes_t16_bytes(M, K));
-    else if (act == ACT_MXFP8 && !prequantized)         // row-major, chunked GEMV for long K
-        *bytes = (size_t)(round256(M * padded_k(K)) + round256(M * (padded_k(K) / 32)));
-    else if (act == ACT_MXFP8 && gemm)                  // row-major input restaged into T16
-        *bytes = (size_t)(round256(mx::act_t16_data_bytes(M, K)) + mx::act_codes_t16_bytes(M, K));
+    *bytes = linear_bytes(elem, N, K, M, act, prequantized != 0, use_gemm(act, M));
     return MX_OK;
 }
 
@@ -419,11 +425,10 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
         if (!aligned16(xq) || !aligned16(xcodes)) return MX_ERR_ALIGN;
     }
     if ((incall || t16) && mx::act_t16_data_bytes(M, K) > kMaxRsrc) return MX_ERR_SHAPE;
-    size_t need = 0;
-    mx_linear_workspace(elem, layout, N, K, M, act, incall ? 0 : 1, &need);
+    const bool gemm = use_gemm(act, M);
+    const size_t need = linear_bytes(elem, N, K, M, act, !incall, gemm);
     if (need > 0 && (!ws || ws_bytes < need)) return MX_ERR_WORKSPACE;
     if (need > 0 && !aligned16(ws)) return MX_ERR_ALIGN;
-    const bool gemm = use_gemm(act, M);
     if (gemm && (N * Kp > kMaxRsrc || M * ldy * 2 > kMaxRsrc)) return MX_ERR_SHAPE;
     if ((st = device_ok()) != MX_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -60,7 +60,27 @@ def _adapters(L):
         assert status == 0 and written.value == need.value, (before, status, written.value)
 
 
+def test_linear(host_lib):
+    """The workspace of a pre-quantized prompt is 0 with the mode on, where the
+    GEMV reads the rows as they are, and a restaged copy with it off."""
+    lines = [ln for ln in child(host_lib, "linear").splitlines() if ln.startswith("mx: linear")]
+    assert len(lines) == 2 and "gemv" in lines[0] and "gemm_w8a8_kernel" in lines[1], lines
+
+
+def _linear(L):
+    switch, need, M = C.c_int.in_dll(L, "mx_switch_to"), C.c_size_t(), 100
+    for before in (1, 0):
+        switch.value = -1
+        L.mx_set_batch_invariant(before)
+        assert L.mx_linear_workspace(0, 0, 512, 1024, M, 1, 1, C.byref(need)) == 0
+        assert (need.value == 0) == (before == 1)
+        switch.value = 1 - before
+        status = L.mx_linear(0, 0, 512, 1024, A(0), A(1), M, 1, 0, None, 0, A(2), 1024, A(3), 32,
+                             None, A(4), 512, A(5) if need.value else None, need.value, None)
+        assert status == 0
+
+
 if __name__ == "__main__":
     mx.LIB_PATH = sys.argv[1]
-    {"adapters": _adapters}[sys.argv[2]](mx.lib())
+    {"adapters": _adapters, "linear": _linear}[sys.argv[2]](mx.lib())
     print(sys.argv[2], "ok")
