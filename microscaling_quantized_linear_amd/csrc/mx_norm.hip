@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(64 * kRowWaves) add_rms_norm_kernel(NormArgs p
                              __uint_as_float(wt[i][d] << 16);
             const float hi = __uint_as_float(v[i][d] & 0xFFFF0000u) * scale *
                              __uint_as_float(wt[i][d] & 0xFFFF0000u);
-            o[d] = live ? bf16_bits(lo) | bf16_bits(hi) << 16 : 0u;   // padding rows: +0
+            // padding rows, and values past K (which the scale of a row that is not
+            // finite would turn into NaN): +0
+            o[d] = live && k0 < K ? bf16_bits(lo) | bf16_bits(hi) << 16 : 0u;
         }
         if (p.y) store16(yr, o, (uint32_t)(2 * k0));
         if (ACT == ACT_BF16) continue;
