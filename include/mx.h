@@ -390,8 +390,8 @@ mx_status mx_moe_down(int elem, int64_t E, int64_t H, int64_t inter,
  *   act MX_ACT_MXFP8      xq [M, ldq] and xcodes [M, ldc], as mx_quant_act of y
  *   act MX_ACT_MXFP8_T16  xq and xcodes of mx_act_t16_sizes' sizes, every byte
  *                         written, as mx_quant_act_t16 of y
- * The bytes and codes are exactly those calls' on the bf16 y.  A row's outputs do not
- * depend on M.
+ * The bytes and codes are exactly those calls' on the bf16 y, also where a value
+ * of y is infinite or NaN.  A row's outputs do not depend on M.
  *   x        (device) bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K
  *   residual (device, nullable) bf16 [M, ldr], the same rules
  *   weight   (device) bf16 [K], 16-byte aligned
