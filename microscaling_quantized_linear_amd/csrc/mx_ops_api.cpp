@@ -17,7 +17,13 @@ struct Span {
     uintptr_t end() const { return begin() + (uintptr_t)(((rows - 1) * ld + cols) * size); }
 };
 bool overlap(const Span &a, const Span &b) {
-    return a.p && b.p && a.begin() < b.end() && b.begin() < a.end();
+    if (!a.p || !b.p || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+    // two column ranges of one wide buffer: rows of the same pitch whose columns
+    // do not meet (b's start d bytes behind a's, counted round the pitch)
+    const uintptr_t pitch = (uintptr_t)(a.ld * a.size);
+    if (pitch == 0 || pitch != (uintptr_t)(b.ld * b.size)) return true;
+    const uintptr_t d = (b.begin() % pitch + pitch - a.begin() % pitch) % pitch;
+    return d < (uintptr_t)(a.cols * a.size) || pitch - d < (uintptr_t)(b.cols * b.size);
 }
 // an output that may stand exactly on an input (each value is read before its
 // place is written) but not elsewhere in it

@@ -3,8 +3,10 @@ rows that are not finite, tile forms and remainders, buffers that share a row.""
 import numpy as np
 import pytest
 
-import oracle
-from test_gpu_ops import BF16, MXFP8, T16, bf16, check_norm, g, mx, rng, run_norm  # noqa: F401
+import ops_ref as ref
+from microscaling_quantized_linear_amd import workloads as wl
+from test_gpu_ops import (BF16, MXFP8, NAN16, T16, bf16, bytes_, check_norm, g,  # noqa: F401
+                          lora_inputs, mx, rng, run_grouped, run_lora, run_norm, split, weight)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +58,81 @@ def test_norm_bytes_of_rows_that_are_not_finite(g, mx, K, rule, act):
     else:
         wq, wc = g.quant(y, rule)
     assert np.array_equal(c, wc) and np.array_equal(q, wq)
+
+
+# ---- column ranges of one wide buffer -----------------------------------------------
+
+
+def wide(g, rows, cols, **parts):
+    """A device buffer [rows, cols] of NaN with arrays in its columns, by their
+    first column; returns the buffer and column views (tensors)."""
+    buf = np.full((rows, cols), NAN16, np.uint16)
+    for name, (at, a) in parts.items():
+        if a is not None:
+            buf[:a.shape[0], at:at + a.shape[1]] = a
+    buf = g.dev(buf)
+    return buf, {name: buf[:, at:] for name, (at, _) in parts.items()}
+
+
+@pytest.mark.parametrize("M", [3, 700])
+def test_norm_in_columns_of_one_buffer(g, mx, M):
+    """x, the residual, the sum and y side by side: the separate buffers' values,
+    and nothing between them written."""
+    import torch
+    K = 96
+    r = rng(80, M)
+    x, res, w = bf16(r, M, K), bf16(r, M, K), bf16(r, K)
+    want = run_norm(g, mx, x, res, w, 1e-6, BF16, 0)
+    buf, v = wide(g, M, 424, x=(0, x), s=(96, None), res=(192, res), y=(320, None))
+    mx.mx_add_rms_norm(M, K, v["x"], 424, v["res"], 424, g.dev(w), 1e-6, BF16, 0, v["s"], 424,
+                       v["y"], 424, None, 0, None, 0)
+    torch.cuda.synchronize()
+    h = g.host_u16(buf)
+    assert np.array_equal(h[:, :96], x) and np.array_equal(h[:, 192:288], res)
+    assert np.array_equal(h[:, 96:192], want[0]) and np.array_equal(h[:, 320:416], want[1])
+    assert (h[:, 288:320] == NAN16).all() and (h[:, 416:] == NAN16).all()
+
+
+@pytest.mark.parametrize("M", [20, 600])
+def test_adapters_in_columns_of_one_buffer(g, mx, M):
+    """x, base and y side by side."""
+    import torch
+    L, R, N, K = 5, 24, 80, 96
+    a, b, s, x, ids, base = lora_inputs(rng(81, M), L, R, N, K, M, "mixed")
+    want = run_lora(g, mx, a, b, s, x, ids, base)
+    buf, v = wide(g, M, 264, x=(0, x), y=(96, None), base=(184, base))
+    need = mx.mx_lora_workspace(L, R, N, K, M)
+    mx.mx_lora_add(L, R, N, K, g.dev(a), g.dev(b), g.dev(s), M, v["x"], 264, g.dev(ids), v["base"],
+                   264, v["y"], 264, bytes_(g, need, fill=0xFF), need)
+    torch.cuda.synchronize()
+    h = g.host_u16(buf)
+    assert np.array_equal(h[:, 96:176], want) and np.array_equal(h[:, :96], x)
+    assert np.array_equal(h[:, 184:], base) and (h[:, 176:184] == NAN16).all()
+
+
+@pytest.mark.parametrize("M", [20, 900])
+@pytest.mark.parametrize("epi", [0, 1])
+def test_grouped_and_combine_in_columns_of_one_buffer(g, mx, M, epi):
+    """The grouped product's x and y side by side, then the combine's ys and y."""
+    import torch
+    E, N, K = 3, 128, 160
+    width = N // 2 if epi else N
+    r = rng(82, M)
+    w, codes, packed = weight(g, r, 0, 0, E, N, K)
+    x, offsets = wl.activations(r, (M, K), 0.01), split(r, M, E, "skew")
+    want = run_grouped(g, mx, 0, 0, E, N, K, packed, offsets, M, x=x, epi=epi)
+    ld = K + width + width + 24
+    buf, v = wide(g, M, ld, x=(0, x), y=(K, None), out=(K + width, None))
+    need = mx.mx_grouped_workspace(0, 0, E, N, K, M, MXFP8, 0)
+    mx.mx_grouped_linear(0, 0, E, N, K, *packed, M, g.dev(offsets), MXFP8, 0, M, v["x"], ld, None,
+                         0, None, 0, None, epi, v["y"], ld, bytes_(g, need), need)
+    T, topk = M // 4, 3
+    pos = r.integers(-1, M, (T, topk)).astype(np.int32)
+    wts = r.random((T, topk)).astype(np.float32)
+    mx.mx_moe_combine(T, topk, width, M, v["y"], ld, g.dev(pos), g.dev(wts), v["out"], ld)
+    torch.cuda.synchronize()
+    h = g.host_u16(buf)
+    assert np.array_equal(h[:, K:K + width], want) and np.array_equal(h[:, :K], x)
+    out, tol = ref.combine(want, pos, wts)
+    ref.assert_within(h[:T, K + width:K + 2 * width], out, tol, "combine")
+    assert (h[T:, K + width:] == NAN16).all() and (h[:, K + 2 * width:] == NAN16).all()
