@@ -321,7 +321,8 @@ SHAPES = [  # E, N, K, M, split
     (16, 128, 640, 33, "skew"), (2, 544, 416, 700, "skew"), (3, 1024, 768, 1500, "even"),
     # enough weight panels for the tiled form at few rows, and for its 256-row tiles
     (130, 48 + 16, 544, 1300, "skew"), (64, 544, 1056, 640, "even"), (140, 32, 2080, 2000, "one"),
-    (512, 32, 96, 4000, "skew"), (300, 288, 160, 2500, "skew"), (520, 64, 1184, 9000, "even")]
+    (512, 32, 96, 4000, "skew"), (300, 288, 160, 2500, "skew"), (520, 64, 1184, 9000, "even"),
+    (130, 288, 160, 17000, "even")]
 
 
 @pytest.mark.parametrize("elem,layout", FORMS)
