@@ -197,11 +197,26 @@ static hipError_t launch_stream(const GroupedArgs &a, hipStream_t st) {
 //   the same, e2m1        44/50/50     55/55/54     57/56/56     218/92/82
 //   E 24, 4096 x 1568     29/31/31     37/31        41/32/32
 //   E 64, 512 x 2048      14/17/17                  23/18/18     75/21/28
-// and with fewer weight panels (of 256 rows) than half the compute units, where
-// the tiled form leaves the others idle:
-//   an expert's rows      64           128          192       256        1024
-//   E 1, 4096 x 4096      9/23/23      16/23/24     22/24     29/24/39   108/27/42
-//   E 8, 1024 x 1024      7/10/10      8/11/11      12/12                (512: 29/13/18)
+// With fewer weight panels (of 256 rows) than half the compute units the tiled
+// form's time is that of one tile, whatever the rows, until its tiles fill the
+// chip.  The streaming form's grows with the batches of 64 rows, and with the
+// panels where these are more than about 28 (streaming / 128; the 256-row tiles
+// are slower up to 256 rows):
+//   panels, batches of 64 rows    1        2        3        4
+//   K 4096, e4m3   16             9/23     16/24    22/24    29/24
+//                  32             13/23    21/24    30/25    38/25
+//                  48             19/23    33/25    47/25    61/26
+//                  64             22/24    37/25    51/26    66/26
+//                  96             30/25    53/26    74/28    96/30
+//                  120            36/27    64/28    92/33    121/34
+//   the same, e2m1 16             8/21     13/22    18/22    23/22
+//                  48             13/22    24/23    33/24    42/24
+//                  96             22/22    38/24    54/25    70/27
+//   K 1024, e4m3   16             7/10     8/11     11/11    14/11
+//                  48             8/10     14/11    21/12    27/12
+//                  96             13/11    24/12    33/13    42/14
+// They meet near 90 panel batches, and batches of at most 16 rows, whose
+// products cost little, stream at any of these panels (96: 22/24, 120: 24/27).
 // MX_GROUPED_FORM (1 to 3) overrides the rule (tuning sweeps only; read once).
 static int grouped_form(const GroupedArgs &a) {
     static const int forced = [] {
@@ -212,7 +227,8 @@ static int grouped_form(const GroupedArgs &a) {
     if (forced >= 1 && forced <= 3) return forced - 1;
     const int64_t rows = a.M / a.E;                       // an expert's rows, on average
     const int64_t panels = a.E * ((a.N + 255) / 256);
-    if (rows <= (panels < 128 ? 192 : 6)) return 0;
+    if (rows <= (panels < 128 ? 16 : 6)) return 0;
+    if (panels < 128 && (rows + 63) / 64 * (panels < 28 ? 28 : panels) <= 90) return 0;
     return rows >= 128 && panels * ((rows + 255) / 256) >= 256 ? 2 : 1;
 }
 

@@ -84,6 +84,22 @@ def test_forms(g):
     assert forms_of(calls) == want
 
 
+def test_form_of_few_weight_panels(g):
+    """Fewer weight panels than half the compute units: streamed while that takes
+    less than one tile does, up to about 90 panel batches of 64 rows; 16 rows an
+    expert always."""
+    stream, tiled = "grouped_stream_kernel", "grouped_gemm_kernel 128-row tiles"
+    cases = [  # E, N, rows an expert, form
+        (8, 3840, 8, stream), (8, 3840, 16, stream), (8, 3840, 64, tiled), (8, 3840, 128, tiled),
+        (8, 3840, 190, tiled), (12, 2048, 16, stream), (12, 2048, 64, tiled),
+        (8, 2048, 64, stream), (8, 2048, 128, tiled), (6, 2048, 64, stream), (6, 2048, 96, tiled),
+        (8, 1024, 128, stream), (8, 1024, 192, tiled), (1, 4096, 192, stream),
+        (1, 4096, 256, tiled), (1, 256, 150, stream), (1, 256, 300, tiled)]
+    calls = [(elem, layout, E, N, 512, E * rows) for E, N, rows, _ in cases
+             for elem, layout in FORMS]
+    assert forms_of(calls) == [form for *_, form in cases for _ in FORMS]
+
+
 def _trace(calls):
     """In a child process with the trace on: each call, without a row to compute."""
     import torch
