@@ -13,11 +13,13 @@
 //           tokens), K split over workgroups and, in each, over eight
 //           wavefronts; the partial sums stay in fp32 in the workspace, added
 //           in a fixed order.
-//   expand  v as the sum of two bf16 numbers (its rounding and the rounding's
-//           remainder, 16 significant bits), each with a product of its own
-//           against the same registers of B: v loses nothing that the bf16
-//           result would show, and B is read once.  The projection is added in
-//           fp32 and y rounded once.
+//   expand  v as the sum of two bf16 numbers (its first eight significant bits
+//           and the remainder's rounding, 16 in all), each with a product of its
+//           own against the same registers of B: v loses nothing that the bf16
+//           result would show, and B is read once.  Cut rather than rounded, the
+//           first number leaves a remainder of its own sign: where its products
+//           overflow, the remainder's cannot be the opposite infinity.  The
+//           projection is added in fp32 and y rounded once.
 // Bounds: at decode the adapters' bytes, 2 R (N + K) each, and two launches'
 // latency; at prefill x, base and y, 2 K + 4 N bytes a row.
 #include "mx_device.h"
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(64 * expand_waves(MT)) lora_expand_kernel(Lora
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float v = s[i] * scale;
-                hi[i] = bf16_bits(v);
+                hi[i] = __float_as_uint(v) >> 16;
                 // (an infinity has no remainder: inf - inf would be NaN)
                 lo[i] = (hi[i] & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(v - bf16_to_f32(hi[i]));
             }

@@ -60,6 +60,29 @@ def test_norm_bytes_of_rows_that_are_not_finite(g, mx, K, rule, act):
     assert np.array_equal(c, wc) and np.array_equal(q, wq)
 
 
+# ---- adapters -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("R", [8, 24, 64, 72])
+@pytest.mark.parametrize("M", [20, 600])
+def test_adapters_beyond_the_range(g, mx, M, R):
+    """Finite inputs whose products leave fp32's range: infinities of the result's
+    sign (no sum here holds both signs), not NaN; the columns beside them are as
+    ever."""
+    L, N, K = 5, 64, 96
+    a, b, s, x, ids, base = lora_inputs(rng(72, M, R), L, R, N, K, M, "each")
+    # A in [1, 2), x in [2^8, 2^9): v beyond 2^13, its remainder's products overflow too
+    a, x = a & 0x007F | 0x3F80, x & 0x007F | 0x4380
+    b = b & 0x7FFF | 0x0080
+    up, down = np.arange(1, N, 7), np.arange(3, N, 7)
+    out, tol = ref.lora(x, a, b, s, ids, base)
+    b[:, up], b[:, down] = 0x7F00, 0xFF00                 # +-2^127
+    y = run_lora(g, mx, a, b, s, x, ids, base)
+    assert (y[:, up] == 0x7F80).all() and (y[:, down] == 0xFF80).all()
+    rest = np.setdiff1d(np.arange(N), np.concatenate([up, down]))
+    ref.assert_within(y[:, rest], out[:, rest], tol[:, rest], "lora")
+
+
 # ---- column ranges of one wide buffer -----------------------------------------------
 
 
