@@ -531,8 +531,10 @@ mx_status mx_lora_workspace(int64_t L, int64_t R, int64_t N, int64_t K, int64_t 
  * 1 <= M <= 4000000; one adapter's A and B and 64 rows of x, base and y stay
  * below 2 GiB; N <= 16776960, K <= 2^26.  Other overlaps of y or ws:
  * MX_ERR_UNSUPPORTED.  Asynchronous, allocates nothing; calls that share a
- * workspace must be ordered.  The order of summation changes at M = 512, unless
- * the batch-invariant mode is on (it changes the workspace's size too). */
+ * workspace must be ordered.  Below 512 rows the order of summation is fixed by K
+ * and R alone; from 512 rows on K is split by M too, so that a row's last bits can
+ * change with the number of rows.  In the batch-invariant mode the order below
+ * 512 rows serves every M (the workspace's size depends on the mode too). */
 mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a, const void *b,
                       const float *scales, int64_t M, const void *x, int64_t ldx,
                       const int32_t *ids, const void *base, int64_t ldb, void *y, int64_t ldy,
@@ -546,8 +548,10 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
  * M > 64 runs the prefill GEMM, which sums in another order.  With the mode
  * on, W8A8 runs the GEMV for every M: every row's output is then bit-identical
  * to the same row computed in any other call, at the cost of re-reading the
- * weights once per 16 rows.  Process-wide and read at each call; set it before
- * sizing workspaces (mx_linear_workspace depends on it).  The environment
+ * weights once per 16 rows.  mx_grouped_linear and mx_lora_add follow the mode
+ * too, each as described there.  Process-wide and read once at each call; set it
+ * before sizing workspaces (mx_linear_workspace and mx_lora_workspace depend on
+ * it).  The environment
  * variable MX_BATCH_INVARIANT=1 turns it on at start-up.  Returns the previous
  * setting (0 or 1). */
 int mx_set_batch_invariant(int on);
