@@ -230,7 +230,7 @@ struct LoraArgs {
     int64_t ldb;
     uint16_t *y;
     int64_t ldy;
-    float *ws;                     // [splits][M][R] partial products x A^T
+    float *ws;                     // [splits][M][R rounded up to 16] partial products x A^T
     bool invariant;                // the form whose order of summation K alone fixes
 };
 constexpr int64_t kLoraMaxRank = 256;
