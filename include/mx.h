@@ -488,7 +488,11 @@ mx_status mx_grouped_workspace(int elem, int layout, int64_t E, int64_t N, int64
  * Asynchronous, allocates nothing, may be captured in a graph; calls that share
  * a workspace must be ordered.  The order of summation of an output depends on
  * M, E and N too (two kernels serve the op), unless the batch-invariant mode is
- * on: then it is fixed by K alone, at the decode kernel's speed. */
+ * on: then it is fixed by K alone, at the decode kernel's speed.
+ * The kernel is chosen by M / E, as the host does not see the offsets: its speed
+ * assumes that M is close to offsets[E] and the rows are spread over the experts.
+ * With few rows an expert on average but most of them on one, that expert's
+ * weights are read again for every 16 to 64 of its rows. */
 mx_status mx_grouped_linear(int elem, int layout, int64_t E, int64_t N, int64_t K,
                             const void *w_packed, const void *codes_packed, int64_t M,
                             const int32_t *offsets, int act, int rule, int64_t xrows,
@@ -555,15 +559,14 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
  * weights once per 16 rows.  mx_grouped_linear and mx_lora_add follow the mode
  * too, each as described there.  Process-wide and read once at each call; set it
  * before sizing workspaces (mx_linear_workspace and mx_lora_workspace depend on
- * it).  The environment
- * variable MX_BATCH_INVARIANT=1 turns it on at start-up.  Returns the previous
- * setting (0 or 1). */
+ * it).  The environment variable MX_BATCH_INVARIANT=1 turns it on at start-up.
+ * Returns the previous setting (0 or 1). */
 int mx_set_batch_invariant(int on);
 
 /* Static description of a status code (never NULL).
  * Dispatch trace: with the environment variable MX_LOG=1 (read once per
- * process) mx_linear and the MoE entry points write one line to stderr for
- * every kernel they launch, naming the kernel, its launch plan and the
+ * process) mx_linear, the MoE entry points and the operators around the linear
+ * write one line to stderr for every kernel they launch, naming the kernel, its launch plan and the
  * shape. */
 const char *mx_status_str(mx_status status);
 
