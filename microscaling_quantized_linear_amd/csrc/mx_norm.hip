@@ -19,7 +19,8 @@
 // layout: a lane pair writes 16 contiguous bytes of it.
 // x, the residual and the stored sum go past the caches (the sum is next read a
 // layer later): M = 4096, K = 7168 with every output, 265 MB, 48.5 -> 42.5 us,
-// 6.2 TB/s; y and the bytes, which the next product reads, do not.
+// 6.2 TB/s (T16 output without y, 207 MB: 55.5 us, its stores are 16-byte pieces of
+// lines that eight XCDs share); y and the bytes, which the next product reads, do not.
 // The order of the sum of squares is fixed by K: a lane's values, the eight
 // wavefronts as a tree, then the 64 lanes.  A row's result is therefore the same
 // in any call.
