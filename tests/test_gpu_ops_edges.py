@@ -5,8 +5,8 @@ import pytest
 
 import ops_ref as ref
 from microscaling_quantized_linear_amd import workloads as wl
-from test_gpu_ops import (BF16, MXFP8, NAN16, T16, bf16, bytes_, check_norm, g,  # noqa: F401
-                          lora_inputs, mx, rng, run_grouped, run_lora, run_norm, split, weight)
+from test_gpu_ops import (BF16, MXFP8, NAN16, T16, Layer, bf16, bytes_, check_norm,  # noqa: F401
+                          g, lora_inputs, mx, rng, run_grouped, run_lora, run_norm, split, weight)
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,64 @@ def test_grouped_and_combine_in_columns_of_one_buffer(g, mx, M, epi):
     out, tol = ref.combine(want, pos, wts)
     ref.assert_within(h[:T, K + width:K + 2 * width], out, tol, "combine")
     assert (h[T:, K + width:] == NAN16).all() and (h[:, K + 2 * width:] == NAN16).all()
+
+
+# ---- together ---------------------------------------------------------------------
+
+
+def test_two_streams_at_once(g, mx):
+    """Two layers with workspaces of their own, on two streams at the same time."""
+    import torch
+    layers = [Layer(g, mx, T, key=k) for k, T in enumerate((700, 40))]
+    want = []
+    for layer in layers:
+        layer.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in layer.outputs()])
+        for t in layer.outputs():
+            t.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(5):
+        for layer, stream in zip(layers, streams):
+            with torch.cuda.stream(stream):
+                layer.run()
+    torch.cuda.synchronize()
+    for layer, outputs in zip(layers, want):
+        layer.check()
+        for x, y in zip(layer.outputs(), outputs):
+            assert torch.equal(x, y)
+
+
+def test_captured_prompt(g, mx):
+    """Prompt sizes captured: the tiled forms, the sort's two launches and the
+    64-row adapters, replayed with other inputs in the same buffers."""
+    import torch
+    a, b = Layer(g, mx, 1100, key=4), Layer(g, mx, 1100, key=5)
+    a.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        a.run()
+    first = {k: a.d[k].clone() for k in ("x", "ids", "aid")}
+    want = []
+    for k in range(2):                                    # eager, with a's and b's inputs
+        if k:
+            for name in first:
+                a.d[name].copy_(b.d[name])
+        a.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in a.outputs()])
+    for turn in range(4):
+        for name in first:
+            a.d[name].copy_(b.d[name] if turn % 2 else first[name])
+        for t in a.outputs():
+            t.zero_()
+        b.run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(a.outputs(), want[turn % 2]):
+            assert torch.equal(x, y)
+    a.x, a.ids, a.aid = b.x, b.ids, b.aid
+    a.check()
