@@ -9,28 +9,6 @@ namespace {
 
 using namespace mx;
 
-// rows x [cols of ld] buffers of element size `size`
-struct Span {
-    const void *p;
-    int64_t rows, ld, cols, size;
-    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
-    uintptr_t end() const { return begin() + (uintptr_t)(((rows - 1) * ld + cols) * size); }
-};
-bool overlap(const Span &a, const Span &b) {
-    if (!a.p || !b.p || a.begin() >= b.end() || b.begin() >= a.end()) return false;
-    // two column ranges of one wide buffer: rows of the same pitch whose columns
-    // do not meet (b's start d bytes behind a's, counted round the pitch)
-    const uintptr_t pitch = (uintptr_t)(a.ld * a.size);
-    if (pitch == 0 || pitch != (uintptr_t)(b.ld * b.size)) return true;
-    const uintptr_t d = (b.begin() % pitch + pitch - a.begin() % pitch) % pitch;
-    return d < (uintptr_t)(a.cols * a.size) || pitch - d < (uintptr_t)(b.cols * b.size);
-}
-// an output that may stand exactly on an input (each value is read before its
-// place is written) but not elsewhere in it
-bool apart_or_same(const Span &out, const Span &in) {
-    return !overlap(out, in) || (out.p == in.p && out.ld == in.ld);
-}
-
 bool ld_bad(int64_t ld, int64_t cols) { return ld < cols || ld > kMaxLd; }
 
 hipStream_t hip(mx_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
