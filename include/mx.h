@@ -276,6 +276,46 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K,
                     int64_t ldc, const void *bias, void *y, int64_t ldy,
                     void *ws, size_t ws_bytes, mx_stream_t stream);
 
+/* Activations of mx_linear_epilogue: z; max(z, 0); max(z, 0)^2; z / (1 + e^-z);
+ * z Phi(z), Phi the normal distribution; z / 2 (1 + tanh(sqrt(2 / pi)
+ * (z + 0.044715 z^3))). */
+typedef enum {
+    MX_FN_NONE = 0,
+    MX_FN_RELU = 1,
+    MX_FN_RELU2 = 2,
+    MX_FN_SILU = 3,
+    MX_FN_GELU = 4,
+    MX_FN_GELU_TANH = 5
+} mx_fn;
+
+/* mx_linear with what follows it in its epilogue:
+ *   z[m][n] = the product (+ bias[n])                                    in fp32
+ *   gated 0:  y[m][n] = bf16(f(z[m][n]) + residual[m][n])                N columns
+ *   gated 1:  y[m][n] = bf16(f(z[m][2 n]) z[m][2 n + 1] + residual[m][n])  N / 2
+ *             (gate and up rows interleaved, as mx_moe_copies lays them out; the
+ *             bias is of the N rows)
+ * f by fn, everything behind the product in fp32 with one rounding at the end: f is
+ * within 2^-14 of its value, relative, where that is at least 2^-126.
+ *   residual (device, nullable: 0) bf16 [M, ldr], 16-byte aligned, ldr % 8 == 0,
+ *            ldr >= the columns; may be y itself (the same pointer and leading
+ *            dimension)
+ *   y        (device) bf16 [M, ldy], ldy >= the columns
+ * Everything else as mx_linear, with the same kernels and workspace
+ * (mx_linear_workspace); without activation, gate and residual the results are
+ * mx_linear's bit for bit, and z is always summed in its order (the
+ * batch-invariant mode included).
+ * Errors: as mx_linear; also MX_ERR_SHAPE when y, the residual or the weights (K
+ * rounded up to 128) reach 2 GiB, or when more than 1,048,560 rows would run on a
+ * decode kernel (bf16 activations, or the batch-invariant mode);
+ * MX_ERR_UNSUPPORTED for an unknown fn or gated, and when y or the workspace
+ * overlaps another buffer in any other way than named above. */
+mx_status mx_linear_epilogue(int elem, int layout, int64_t N, int64_t K, const void *w_packed,
+                             const void *codes_packed, int64_t M, int act, int rule,
+                             const void *x, int64_t ldx, const void *xq, int64_t ldq,
+                             const void *xcodes, int64_t ldc, const void *bias, int fn, int gated,
+                             const void *residual, int64_t ldr, void *y, int64_t ldy, void *ws,
+                             size_t ws_bytes, mx_stream_t stream);
+
 /* Workspace bytes mx_moe_linear needs: T * topk * N * 4 when topk_weights is
  * used (combine mode), else 0. */
 mx_status mx_moe_workspace(int elem, int64_t E, int64_t N, int64_t K,
@@ -547,6 +587,94 @@ mx_status mx_lora_add(int64_t L, int64_t R, int64_t N, int64_t K, const void *a,
                       const float *scales, int64_t M, const void *x, int64_t ldx,
                       const int32_t *ids, const void *base, int64_t ldb, void *y, int64_t ldy,
                       void *ws, size_t ws_bytes, mx_stream_t stream);
+
+/* ---- Between the products of a layer ---- */
+
+/* Types of router logits and of a residual stream. */
+typedef enum { MX_FLOAT_BF16 = 0, MX_FLOAT_F32 = 1 } mx_float;
+/* A router's scores: softmax over all E experts, or a sigmoid of each. */
+typedef enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 } mx_score;
+
+/* The experts of each token, from its router logits x (mx_moe_sort, mx_moe_linear
+ * and mx_moe_combine take the result):
+ *   s[e] = softmax(x)[e] or sigmoid(x[e]), by score
+ *   c[e] = s[e] + bias[e], a balance that orders but does not weigh; x[e] without a
+ *          bias (the same order as the scores', without their rounding)
+ *   groups of E / groups neighbouring experts: the topk_groups groups with the
+ *          largest sum of their group_best (1 or 2) largest c are kept, equal ones
+ *          by lower number (groups 1: all experts)
+ *   topk_ids     the topk experts of the kept groups with the largest c, descending,
+ *          equal ones by lower number
+ *   topk_weights scale * s of the chosen, with renorm 1 divided by their sum (0
+ *          where that is 0)
+ * With a bias, s is rounded to fp32 from 64 bits, and c and a group's sum in fp32: the
+ * choice is a function of the inputs alone.  An expert whose logit or bias is -inf or
+ * NaN is masked: its s is 0 and it is not chosen; +inf counts as the largest fp32
+ * number.  Choices that find no expert get id -1 and weight 0 (a token whose logits
+ * are all masked has none, as a batch's padding); a group with fewer than group_best
+ * experts left comes behind all others.  A token's results do not depend on
+ * the other tokens or on T.
+ *   type     of the logits (mx_float)
+ *   logits   (device) [T, ldl], aligned to their elements, ldl >= E
+ *   bias     (device, nullable) fp32 [E]
+ *   topk_ids (device) int32 [T, topk]
+ *   topk_weights (device) fp32 [T, topk]
+ * Rules: 1 <= E <= 1024, T >= 1, topk <= 64, T * topk <= 4000000, 1 <= groups <= 64,
+ * E % groups == 0, 1 <= topk_groups <= groups, topk <= topk_groups * (E / groups),
+ * group_best <= E / groups, a finite scale.
+ * Errors: MX_ERR_UNSUPPORTED also for group_best 2 without a bias (zeros will do)
+ * and for outputs that overlap another buffer. */
+mx_status mx_moe_route(int64_t E, int64_t T, int64_t topk, int type, const void *logits,
+                       int64_t ldl, int score, const float *bias, int64_t groups,
+                       int64_t topk_groups, int group_best, int renorm, float scale,
+                       int32_t *topk_ids, float *topk_weights, mx_stream_t stream);
+
+/* The norms behind a block and ahead of the next one, with the block's gate and the
+ * scaled residual stream between them, in one pass:
+ *   p[m][k] = x[m][k] * rsqrt(mean_k x[m][k]^2 + eps) * (offset + post_weight[k])
+ *             (post_weight NULL: p = x)
+ *   s[m][k] = T(alpha * residual[m][k] + gate[g][k] * p[m][k])
+ *             (residual NULL: 0; gate NULL: 1)
+ *   y[m][k] = bf16(s[m][k] * rsqrt(mean_k s[m][k]^2 + eps) * (offset + weight[k]))
+ * in fp32 between the inputs and these roundings (T(), bf16(): to nearest even; p is
+ * not rounded), T the residual stream's type; y is handed out as by mx_add_rms_norm:
+ *   act MX_ACT_BF16       y only
+ *   act MX_ACT_MXFP8      xq [M, ldq] and xcodes [M, ldc], as mx_quant_act of y
+ *   act MX_ACT_MXFP8_T16  xq and xcodes of mx_act_t16_sizes' sizes, every byte
+ *                         written, as mx_quant_act_t16 of y
+ * A row's outputs do not depend on M.
+ *   x        (device) bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K: the
+ *            block's output
+ *   post_weight (device, nullable) bf16 [K], 16-byte aligned
+ *   gate     (device, nullable) bf16 [gates, ldg], the rules of x; g = gate_ids[m], or
+ *            0 without gate_ids; where g is outside [0, gates) the block adds nothing:
+ *            s = T(alpha * residual)
+ *   gate_ids (device, nullable; unused without a gate) int32 [M]
+ *   stream_type  of residual and sum (mx_float)
+ *   residual (device, nullable) [M, ldr], 16-byte aligned, rows a multiple of 16 bytes
+ *            apart
+ *   alpha, offset  finite; offset is 1 where weights are stored around zero
+ *   weight   (device, nullable) bf16 [K], 16-byte aligned; without it there is no second
+ *            norm: act is MX_ACT_BF16, y NULL, and sum is the only output
+ *   eps      >= 0 (0 makes a row of zeros NaN)
+ *   sum      (device, nullable with a weight) [M, lds]: receives s; the residual's rules;
+ *            may be the residual itself, and, with a bf16 stream, x itself (the same
+ *            pointer and leading dimension)
+ *   y        (device; nullable unless act is MX_ACT_BF16) bf16 [M, ldy]; may be x itself,
+ *            and, with a bf16 stream, the residual itself, when sum is not
+ *   xq, xcodes (device; unused when act is MX_ACT_BF16): ldq % 16 == 0,
+ *            ldq >= K, ldc >= K / 32 (ldq, ldc unused for T16); 16-byte aligned
+ *            (xcodes of MX_ACT_MXFP8: any)
+ *   rule     as mx_quant_act (checked for every act)
+ * Rules: 1 <= M <= 4000000, 32 <= K <= 65536, K % 32 == 0, gates <= 4000000.
+ * Errors: MX_ERR_UNSUPPORTED also when an output overlaps another buffer in any other
+ *   way than named above. */
+mx_status mx_block_norm(int64_t M, int64_t K, const void *x, int64_t ldx, const void *post_weight,
+                        const void *gate, int64_t gates, int64_t ldg, const int32_t *gate_ids,
+                        int stream_type, const void *residual, int64_t ldr, float alpha,
+                        const void *weight, float offset, float eps, int act, int rule, void *sum,
+                        int64_t lds, void *y, int64_t ldy, void *xq, int64_t ldq, void *xcodes,
+                        int64_t ldc, mx_stream_t stream);
 
 /* Batch-invariant mode ([rocm_native] process_weights_after_loading: under
  * VLLM_BATCH_INVARIANT the page leaves its block-scaled GEMM, whose split of

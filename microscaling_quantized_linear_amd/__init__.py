@@ -29,6 +29,9 @@ __all__ = [
     "MX_EPI_NONE", "MX_EPI_SILU", "mx_add_rms_norm", "mx_moe_sort_workspace", "mx_moe_sort",
     "mx_grouped_workspace", "mx_grouped_linear", "mx_moe_combine", "mx_lora_workspace",
     "mx_lora_add",
+    "MX_FN_NONE", "MX_FN_RELU", "MX_FN_RELU2", "MX_FN_SILU", "MX_FN_GELU", "MX_FN_GELU_TANH",
+    "mx_linear_epilogue", "MX_FLOAT_BF16", "MX_FLOAT_F32", "MX_SCORE_SOFTMAX", "MX_SCORE_SIGMOID",
+    "mx_moe_route", "mx_block_norm",
 ]
 
 MX_E4M3, MX_E2M1 = 0, 1
@@ -37,6 +40,9 @@ MX_RULE_OCP, MX_RULE_CEIL448 = 0, 1
 MX_ACT_BF16, MX_ACT_MXFP8, MX_ACT_MXFP8_T16 = 0, 1, 2
 MX_PERM_Q_ROWS, MX_PERM_O_COLS = 0, 1
 MX_EPI_NONE, MX_EPI_SILU = 0, 1
+MX_FN_NONE, MX_FN_RELU, MX_FN_RELU2, MX_FN_SILU, MX_FN_GELU, MX_FN_GELU_TANH = range(6)
+MX_FLOAT_BF16, MX_FLOAT_F32 = 0, 1
+MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = 0, 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmx.so")
 _lib = None
@@ -102,6 +108,11 @@ def lib() -> C.CDLL:
                                       p, i64, p, i64, p, i32, p, i64, p, sz, p],
                 "mx_moe_combine": [i64, i64, i64, i64, p, i64, p, p, p, i64, p],
                 "mx_lora_workspace": [i64, i64, i64, i64, i64, C.POINTER(sz)],
+                "mx_linear_epilogue": [i32, i32, i64, i64, p, p, i64, i32, i32, p, i64, p, i64, p,
+                                       i64, p, i32, i32, p, i64, p, i64, p, sz, p],
+                "mx_moe_route": [i64, i64, i64, i32, p, i64, i32, p, i64, i64, i32, i32, f32, p, p, p],
+                "mx_block_norm": [i64, i64, p, i64, p, p, i64, i64, p, i32, p, i64, f32, p, f32, f32,
+                                  i32, i32, p, i64, p, i64, p, i64, p, i64, p],
                 "mx_lora_add": [i64, i64, i64, i64, p, p, p, i64, p, i64, p, p, i64, p, i64, p, sz,
                                 p]}.items():
             # a build of part of the sources (the host checks') may lack these;
@@ -342,3 +353,31 @@ def mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws,
     a, b, scales, x, ids, base, y, ws = _here(a, b, scales, x, ids, base, y, ws)
     _check(lib().mx_lora_add(L, R, N, K, a, b, scales, M, x, ldx, ids, base, ldb, y, ldy, ws,
                              ws_bytes, _raw_stream(stream)), "mx_lora_add")
+
+
+def mx_linear_epilogue(elem, layout, N, K, w_packed, codes_packed, M, act, rule, x, ldx, xq, ldq,
+                       xcodes, ldc, bias, fn, gated, residual, ldr, y, ldy, ws, ws_bytes,
+                       stream=None):
+    w_packed, codes_packed, x, xq, xcodes, bias, residual, y, ws = _here(
+        w_packed, codes_packed, x, xq, xcodes, bias, residual, y, ws)
+    _check(lib().mx_linear_epilogue(elem, layout, N, K, w_packed, codes_packed, M, act, rule, x, ldx,
+                                    xq, ldq, xcodes, ldc, bias, fn, int(gated), residual, ldr, y,
+                                    ldy, ws, ws_bytes, _raw_stream(stream)), "mx_linear_epilogue")
+
+
+def mx_moe_route(E, T, topk, type, logits, ldl, score, bias, groups, topk_groups, group_best, renorm,
+                 scale, topk_ids, topk_weights, stream=None):
+    logits, bias, topk_ids, topk_weights = _here(logits, bias, topk_ids, topk_weights)
+    _check(lib().mx_moe_route(E, T, topk, type, logits, ldl, score, bias, groups, topk_groups,
+                              group_best, int(renorm), scale, topk_ids, topk_weights,
+                              _raw_stream(stream)), "mx_moe_route")
+
+
+def mx_block_norm(M, K, x, ldx, post_weight, gate, gates, ldg, gate_ids, stream_type, residual, ldr,
+                  alpha, weight, offset, eps, act, rule, sum, lds, y, ldy, xq, ldq, xcodes, ldc,
+                  stream=None):
+    x, post_weight, gate, gate_ids, residual, weight, sum, y, xq, xcodes = _here(
+        x, post_weight, gate, gate_ids, residual, weight, sum, y, xq, xcodes)
+    _check(lib().mx_block_norm(M, K, x, ldx, post_weight, gate, gates, ldg, gate_ids, stream_type,
+                               residual, ldr, alpha, weight, offset, eps, act, rule, sum, lds, y, ldy,
+                               xq, ldq, xcodes, ldc, _raw_stream(stream)), "mx_block_norm")

@@ -107,6 +107,8 @@ using mx::ROW32;
 
 // largest M served by the decode GEMV for W8A8; above it the GEMM runs
 constexpr int64_t kGemvMaxM = 64;
+// rows of a GEMV launch: one launch-grid row for each 16 of them
+constexpr int64_t kGemvMaxRows = 16 * 65535;
 
 // the W8A8 prefill GEMM serves this call (else a GEMV); reads the batch-invariant
 // mode, so a call asks once and keeps the answer
@@ -390,17 +392,25 @@ mx_status mx_linear_workspace(int elem, int layout, int64_t N, int64_t K, int64_
     return MX_OK;
 }
 
-mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_packed,
-                    const void *codes_packed, int64_t M, int act, int rule, const void *x,
-                    int64_t ldx, const void *xq, int64_t ldq, const void *xcodes, int64_t ldc,
-                    const void *bias, void *y, int64_t ldy, void *ws, size_t ws_bytes,
-                    mx_stream_t stream) {
+// The product behind mx_linear (end null) and mx_linear_epilogue, whose enums and
+// largest sizes are checked already.
+struct LinearEnd {
+    int fn, gated;
+    const void *residual;
+    int64_t ldr;
+};
+static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const void *w_packed,
+                     const void *codes_packed, int64_t M, int act, int rule, const void *x,
+                     int64_t ldx, const void *xq, int64_t ldq, const void *xcodes, int64_t ldc,
+                     const void *bias, const LinearEnd *end, void *y, int64_t ldy, void *ws,
+                     size_t ws_bytes, mx_stream_t stream) {
     mx_status st = shape_ok(elem, layout, 1, N, K);
     if (st != MX_OK) return st;
     if (act != ACT_BF16 && act != ACT_MXFP8 && act != ACT_MXFP8_T16) return MX_ERR_UNSUPPORTED;
     if (rule != mx::RULE_OCP && rule != mx::RULE_CEIL448) return MX_ERR_UNSUPPORTED;
     if (elem == E2M1 && (layout != ROW32 || act != ACT_BF16)) return MX_ERR_UNSUPPORTED;
-    if (M < 1 || ldy < N) return MX_ERR_SHAPE;
+    const int64_t width = end && end->gated ? N / 2 : N;
+    if (M < 1 || ldy < width) return MX_ERR_SHAPE;
     if (!w_packed || !codes_packed || !y) return MX_ERR_NULL;
     if (!aligned16(w_packed) || !aligned16(codes_packed) || !aligned16(y) || ldy % 8 != 0)
         return MX_ERR_ALIGN;
@@ -430,6 +440,36 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
     if (need > 0 && (!ws || ws_bytes < need)) return MX_ERR_WORKSPACE;
     if (need > 0 && !aligned16(ws)) return MX_ERR_ALIGN;
     if (gemm && (N * Kp > kMaxRsrc || M * ldy * 2 > kMaxRsrc)) return MX_ERR_SHAPE;
+    mx::EpiArgs fin{};
+    if (end) {
+        const void *res = end->residual;
+        if (M * ldy * 2 > kMaxRsrc || (!gemm && M > kGemvMaxRows)) return MX_ERR_SHAPE;
+        if (res && (end->ldr < width || M * end->ldr * 2 > kMaxRsrc)) return MX_ERR_SHAPE;
+        if (res && (!aligned16(res) || end->ldr % 8 != 0)) return MX_ERR_ALIGN;
+        size_t wb = 0, cb = 0;
+        if ((st = mx_packed_sizes(elem, layout, 1, N, K, &wb, &cb)) != MX_OK) return st;
+        const mx::Span sy{y, M, ldy, width, 2}, sr{res, M, end->ldr, width, 2};
+        const mx::Span sw{need ? ws : nullptr, 1, 0, (int64_t)need, 1};
+        const mx::Span ins[] = {{w_packed, 1, 0, (int64_t)wb, 1},
+                                {codes_packed, 1, 0, (int64_t)cb, 1},
+                                {act == ACT_BF16 || incall ? x : nullptr, M, ldx, K, 2},
+                                {preq ? xq : nullptr, M, ldq, K, 1},
+                                {preq ? xcodes : nullptr, M, ldc, K / 32, 1},
+                                {t16 ? xq : nullptr, 1, 0, mx::act_t16_data_bytes(M, K), 1},
+                                {t16 ? xcodes : nullptr, 1, 0, mx::act_codes_t16_bytes(M, K), 1},
+                                {bias, 1, 0, N, 2}};
+        for (const mx::Span &in : ins)
+            if (mx::overlap(sy, in) || mx::overlap(sw, in)) return MX_ERR_UNSUPPORTED;
+        if (!mx::apart_or_same(sy, sr) || mx::overlap(sw, sr) || mx::overlap(sw, sy))
+            return MX_ERR_UNSUPPORTED;
+        // without any of it the kernels of mx_linear run
+        fin.on = end->fn != mx::FN_NONE || end->gated || res;
+        fin.fn = end->fn;
+        fin.gated = end->gated;
+        fin.res = static_cast<const uint16_t *>(res);
+        fin.ldr = end->ldr;
+    }
+    const char *with = fin.on ? " with epilogue" : "";
     if ((st = device_ok()) != MX_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     uint8_t *wsp = static_cast<uint8_t *>(ws);
@@ -452,9 +492,10 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
         g.bias = static_cast<const uint16_t *>(bias);
         g.y = static_cast<uint16_t *>(y);
         g.ldy = ldy;
-        log_dispatch("linear: gemv_w8_fused_kernel %s, quantization inside (rule %d), "
+        g.fin = fin;
+        log_dispatch("linear: gemv_w8_fused_kernel %s%s, quantization inside (rule %d), "
                      "%d waves x %d steps x %d tiles; M=%lld N=%lld K=%lld",
-                     layout_name(layout), rule, w8.nw, w8.spw, w8.g, (long long)M, (long long)N,
+                     layout_name(layout), with, rule, w8.nw, w8.spw, w8.g, (long long)M, (long long)N,
                      (long long)K);
         return launched(mx::launch_gemv_w8_fused(layout, rule, g, w8, s));
     }
@@ -499,8 +540,9 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
         g.bias = static_cast<const uint16_t *>(bias);
         g.y = static_cast<uint16_t *>(y);
         g.ldy = ldy;
-        log_dispatch("linear: gemm_w8a8_kernel %s, %d x 256 tiles; M=%lld N=%lld K=%lld",
-                     layout_name(layout), mx::gemm_tile_n(N), (long long)M, (long long)N,
+        g.fin = fin;
+        log_dispatch("linear: gemm_w8a8_kernel %s%s, %d x 256 tiles; M=%lld N=%lld K=%lld",
+                     layout_name(layout), with, mx::gemm_tile_n(N), (long long)M, (long long)N,
                      (long long)K);
         return launched(mx::launch_gemm(layout, g, s));
     }
@@ -514,6 +556,7 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
         g.bias = static_cast<const uint16_t *>(bias);
         g.y = static_cast<uint16_t *>(y);
         g.ldy = ldy;
+        g.fin = fin;
         if (a16) {
             g.xf = aq;
             g.xct = ac;
@@ -523,11 +566,11 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
             g.xc = ac;
             g.ldc = lc;
         }
-        log_dispatch("linear: %s %s, %s activations, %d waves x %d steps x %d tiles; "
+        log_dispatch("linear: %s %s%s, %s activations, %d waves x %d steps x %d tiles; "
                      "M=%lld N=%lld K=%lld",
                      mx::gemv_w8_even(N, K, w8) ? (a16 ? "gemv_w8_even_kernel" : "gemv_w8_rm_kernel")
                                                 : "gemv_w8_kernel",
-                     layout_name(layout), a16 ? "T16" : "row-major", w8.nw, w8.spw, w8.g,
+                     layout_name(layout), with, a16 ? "T16" : "row-major", w8.nw, w8.spw, w8.g,
                      (long long)M, (long long)N, (long long)K);
         return launched(mx::launch_gemv_w8(layout, a16, g, w8, s));
     }
@@ -553,12 +596,44 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_pa
     a.bias = static_cast<const uint16_t *>(bias);
     a.y = static_cast<uint16_t *>(y);
     a.ldy = ldy;
+    a.fin = fin;
     const mx::GemvShape sh = gemv_shape(Kp / 128, false);
-    log_dispatch("linear: gemv_kernel %s %s, %s activations, %d waves x %d-step chunks x %d "
+    log_dispatch("linear: gemv_kernel %s %s%s, %s activations, %d waves x %d-step chunks x %d "
                  "tiles; M=%lld N=%lld K=%lld",
-                 elem_name(elem), layout_name(layout), act == ACT_BF16 ? "bf16" : "row-major MXFP8",
+                 elem_name(elem), layout_name(layout), with, act == ACT_BF16 ? "bf16" : "row-major MXFP8",
                  sh.nw, sh.chunk, sh.tiles, (long long)M, (long long)N, (long long)K);
     return launched(mx::launch_gemv(elem, layout, act, false, a, sh, s));
+}
+
+mx_status mx_linear(int elem, int layout, int64_t N, int64_t K, const void *w_packed,
+                    const void *codes_packed, int64_t M, int act, int rule, const void *x,
+                    int64_t ldx, const void *xq, int64_t ldq, const void *xcodes, int64_t ldc,
+                    const void *bias, void *y, int64_t ldy, void *ws, size_t ws_bytes,
+                    mx_stream_t stream) {
+    return linear_run(elem, layout, N, K, w_packed, codes_packed, M, act, rule, x, ldx, xq, ldq,
+                      xcodes, ldc, bias, nullptr, y, ldy, ws, ws_bytes, stream);
+}
+
+mx_status mx_linear_epilogue(int elem, int layout, int64_t N, int64_t K, const void *w_packed,
+                             const void *codes_packed, int64_t M, int act, int rule, const void *x,
+                             int64_t ldx, const void *xq, int64_t ldq, const void *xcodes,
+                             int64_t ldc, const void *bias, int fn, int gated,
+                             const void *residual, int64_t ldr, void *y, int64_t ldy, void *ws,
+                             size_t ws_bytes, mx_stream_t stream) {
+    mx_status st = shape_ok(elem, layout, 1, N, K);
+    if (st != MX_OK) return st;
+    if (fn < mx::FN_NONE || fn > mx::FN_GELU_TANH || (gated != 0 && gated != 1))
+        return MX_ERR_UNSUPPORTED;
+    // sizes that the rules multiply
+    const bool given = xq && xcodes;
+    if (K > kMaxRsrc || N > kMaxRsrc / padded_k(K) || M > kMaxRsrc || ldy > kMaxRsrc ||
+        (residual && ldr > kMaxRsrc) ||
+        ((act == ACT_BF16 || (act == ACT_MXFP8 && !given)) && ldx > kMaxRsrc) ||
+        (act == ACT_MXFP8 && given && (ldq > kMaxRsrc || ldc > kMaxRsrc)))
+        return MX_ERR_SHAPE;
+    const LinearEnd end{fn, gated, residual, ldr};
+    return linear_run(elem, layout, N, K, w_packed, codes_packed, M, act, rule, x, ldx, xq, ldq,
+                      xcodes, ldc, bias, &end, y, ldy, ws, ws_bytes, stream);
 }
 
 mx_status mx_moe_workspace(int elem, int64_t E, int64_t N, int64_t K, int64_t T, int64_t topk,

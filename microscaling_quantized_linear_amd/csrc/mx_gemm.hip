@@ -29,11 +29,25 @@
 // 4 q + u's code, picked by the MFMA's byte select.  Out-of-range rows, tokens
 // and K tails read zeros through buffer-resource bounds.
 #include "mx_device.h"
+#include "mx_epilogue.h"
 #include "mx_kernels.h"
 
 #include <type_traits>
 
+// mx_gemm_epi.hip compiles this kernel again with an epilogue
+#ifdef MX_WITH_EPILOGUE
+#define MX_LAUNCH(name) name##_epi
+#else
+#define MX_LAUNCH(name) name
+#endif
+
 namespace mx {
+
+#ifdef MX_WITH_EPILOGUE
+constexpr bool kEpi = true;
+#else
+constexpr bool kEpi = false;
+#endif
 
 constexpr int kBM = 256;           // tokens per workgroup
 
@@ -43,7 +57,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 // (instantiated apart so the steady-state copies of whole-step shapes carry
 // no extra mask).  REM: the step count S is not a multiple of eight, so the
 // last iteration of the eight-step loop stops after step S - 1.
-template <int LAYOUT, int NTW, bool TAIL, bool REM>
+template <int LAYOUT, int NTW, bool TAIL, bool REM, bool EPI>
 __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
     constexpr int BN = NTW * 32;
     constexpr int kWBytes = 2 * NTW * 2048;               // one step's weight chunks
@@ -269,7 +283,11 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
 
     // the workgroup's BN bias values, staged in LDS under the first barrier
     // (the bias needs only 2-byte alignment: one element per thread)
-    if (p.bias && tid < BN) bias_lds[tid] = n0 + tid < p.N ? p.bias[n0 + tid] : 0;
+    // (with an epilogue, zeros stand for no bias)
+    if constexpr (EPI) {
+        if (tid < BN) bias_lds[tid] = p.bias && n0 + tid < p.N ? p.bias[n0 + tid] : 0;
+    } else if (p.bias && tid < BN)
+        bias_lds[tid] = n0 + tid < p.N ? p.bias[n0 + tid] : 0;
 
     QScales qa, qb;
     BFrag ba, bb;
@@ -366,6 +384,129 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
         ybase[mt] = m < p.M ? (uint32_t)m * ldy2 + (uint32_t)(n0 + 8 * g) * 2u : kOOB;
     }
     const int64_t nlim = p.N - n0 - 8 * g;                // columns left for this lane's pieces
+    if constexpr (EPI) {
+        // With an epilogue: the sums leave their registers the same way, through
+        // f, the gate and the residual, whose 16-byte pieces are read in the layout
+        // of the stores (a slab ahead) and traded back by the same swaps.  Gated:
+        // rows 2 i and 2 i + 1 give column i, so dword 2 a + g of a slab's eight
+        // holds columns 4 a + 2 g, + 1.
+        const FnCoef fc = fn_coef(p.fin.fn);
+        const uint32_t ldr2 = (uint32_t)p.fin.ldr * 2u;
+        const __amdgpu_buffer_rsrc_t resr =
+            make_rsrc(p.fin.res ? p.fin.res : p.y, p.fin.res ? (uint32_t)(p.M * p.fin.ldr * 2) : 0u);
+        auto finish = [&](auto kindconst, auto gatedconst) {
+            constexpr int KIND = decltype(kindconst)::value;
+            constexpr bool GATED = decltype(gatedconst)::value;
+            constexpr int PC = GATED ? 1 : 2;             // 16-byte pieces a lane, slab and mt
+            uint32_t yb[2], rb[2];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                const int64_t m = m0 + 64 * wave + 32 * mt + rr;
+                const uint32_t c0 = (uint32_t)((GATED ? n0 / 2 : n0) + 8 * g) * 2u;
+                yb[mt] = m < p.M ? (uint32_t)m * ldy2 + c0 : kOOB;
+                rb[mt] = m < p.M ? (uint32_t)m * ldr2 + c0 : kOOB;
+            }
+            // weight rows left for this lane's pieces, and a piece's offset
+            const int64_t left = p.N - n0 - (GATED ? 16 : 8) * g;
+            auto at = [&](uint32_t base, int nt, int pc) -> uint32_t {
+                const int row = 32 * nt + 16 * pc;
+                return row < left ? base + (GATED ? row : 2 * row) : kOOB;
+            };
+            v4u res[2][2][PC];
+            auto fetch = [&](v4u (&r)[2][PC], int nt) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int pc = 0; pc < PC; ++pc) {
+                        const uint32_t off = at(rb[mt], nt, pc);
+                        r[mt][pc] = load16(resr, off | (off & kOOB));
+                    }
+            };
+            fetch(res[0], 0);
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt) {
+                if (nt + 1 < NTW) fetch(res[(nt + 1) % 2], nt + 1);
+                v2u bias2[4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+                    bias2[a] = *reinterpret_cast<const v2u *>(bias_lds + 32 * nt + 8 * a + 4 * g);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const v16f &c = acc[nt][mt];
+                    auto z = [&](int i) {
+                        const uint32_t b = bias2[i / 4][i / 2 % 2];
+                        return c[i] + (i % 2 ? __uint_as_float(b & 0xFFFF0000u)
+                                             : __uint_as_float(b << 16));
+                    };
+                    auto lo16 = [](uint32_t v) { return __uint_as_float(v << 16); };
+                    auto hi16 = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
+                    if constexpr (GATED) {
+                        const v4u r = res[nt % 2][mt][0];
+                        const auto r02 = __builtin_amdgcn_permlane32_swap(r[0], r[1], false, false);
+                        const auto r13 = __builtin_amdgcn_permlane32_swap(r[2], r[3], false, false);
+                        const uint32_t rd[4] = {r02[0], r13[0], r02[1], r13[1]};
+                        uint32_t d[4];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            d[a] = pk(fn_value<KIND>(z(4 * a), fc) * z(4 * a + 1) + lo16(rd[a]),
+                                      fn_value<KIND>(z(4 * a + 2), fc) * z(4 * a + 3) + hi16(rd[a]));
+                        const auto s02 = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+                        const auto s13 = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+                        const uint32_t off = at(yb[mt], nt, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(v4u{s02[0], s02[1], s13[0], s13[1]}, yr,
+                                                               (int)(off | (off & kOOB)), 0, 0);
+                    } else {
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) {
+                            const v4u r = res[nt % 2][mt][pc];
+                            uint32_t o[2][2], rd[2][2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const auto sw = __builtin_amdgcn_permlane32_swap(r[h], r[2 + h], false,
+                                                                                 false);
+                                rd[0][h] = sw[0];
+                                rd[1][h] = sw[1];
+                            }
+#pragma unroll
+                            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int i = 4 * (2 * pc + d) + 2 * h;
+                                    o[d][h] = pk(fn_value<KIND>(z(i), fc) + lo16(rd[d][h]),
+                                                 fn_value<KIND>(z(i + 1), fc) + hi16(rd[d][h]));
+                                }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const auto sw = __builtin_amdgcn_permlane32_swap(o[0][h], o[1][h], false,
+                                                                                 false);
+                                o[0][h] = sw[0];
+                                o[1][h] = sw[1];
+                            }
+                            const uint32_t off = at(yb[mt], nt, pc);
+                            __builtin_amdgcn_raw_buffer_store_b128(
+                                v4u{o[0][0], o[0][1], o[1][0], o[1][1]}, yr,
+                                (int)(off | (off & kOOB)), 0, 0);
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);        // one slab at a time, as below
+            }
+        };
+        using K0 = std::integral_constant<int, KIND_SIMPLE>;
+        using K1 = std::integral_constant<int, KIND_LOGISTIC>;
+        using K2 = std::integral_constant<int, KIND_ERF>;
+        const int kind = fn_kind(p.fin.fn);
+        if (p.fin.gated) {
+            if (kind == KIND_SIMPLE) finish(K0{}, std::true_type{});
+            else if (kind == KIND_LOGISTIC) finish(K1{}, std::true_type{});
+            else finish(K2{}, std::true_type{});
+        } else {
+            if (kind == KIND_SIMPLE) finish(K0{}, std::false_type{});
+            else if (kind == KIND_LOGISTIC) finish(K1{}, std::false_type{});
+            else finish(K2{}, std::false_type{});
+        }
+        return;
+    }
     auto epilogue = [&](auto biasconst) {
         constexpr bool kBias = decltype(biasconst)::value;
 #pragma unroll
@@ -428,22 +569,25 @@ static hipError_t launch_ntw(const GemmArgs &a, hipStream_t st) {
     const dim3 grid((unsigned)tiles), block(256);
     const bool tail = a.K % 128 != 0, rem = (a.K + 127) / 128 % 8 != 0;
     if (tail)
-        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, true, true>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, true, true, kEpi>), grid, block, 0, st, a);
     else if (rem)
-        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, false, true>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, false, true, kEpi>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, false, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_w8a8_kernel<LAYOUT, NTW, false, false, kEpi>), grid, block, 0, st, a);
     return hipGetLastError();
 }
 
+#ifndef MX_WITH_EPILOGUE
 int gemm_tile_n(int64_t N) {
     // 224-row tiles when they divide N evenly into a multiple of 8 bands
     // (7168 = 32 x 224: 512 tiles at M = 4096, two per CU); 256 otherwise
     if (N % 224 == 0 && (N / 224) % 8 == 0) return 224;
     return 256;
 }
+#endif
 
-hipError_t launch_gemm(int layout, const GemmArgs &a, hipStream_t st) {
+hipError_t MX_LAUNCH(launch_gemm)(int layout, const GemmArgs &a, hipStream_t st) {
+    if (!kEpi && a.fin.on) return launch_gemm_epi(layout, a, st);
     const int bn = gemm_tile_n(a.N);
     if (layout == ROW32)
         return bn == 224 ? launch_ntw<ROW32, 7>(a, st) : launch_ntw<ROW32, 8>(a, st);

@@ -29,6 +29,7 @@
 // silu(gate) * up, one output per pair ([weights942] moe_copies interleaves
 // the two halves: even rows gate, odd rows up).
 #include "mx_device.h"
+#include "mx_epilogue.h"
 #include "mx_kernels.h"
 
 namespace mx {
@@ -110,7 +111,8 @@ __device__ inline v4f a16_exact_tile(v4f acc, v4u a0, v4u a1, v4u x0, v4u x1,
 // With NW = 2 (the K = 1536 down projection) three wavefronts per SIMD keep
 // its ~1,500 workgroups resident too, and leave the registers that sharing
 // the code dwords of a chunk needs (47.2 against 48.1 us for the MoE block).
-template <int ELEM, int LAYOUT, int ACT, bool MOE, int NW, int P, int G>
+// EPI: with an epilogue (dense only; mx_gemv_epi.hip compiles those).
+template <int ELEM, int LAYOUT, int ACT, bool MOE, int NW, int P, int G, bool EPI>
 __global__ void __launch_bounds__(NW * 64)
 __attribute__((amdgpu_waves_per_eu(MOE && ELEM == E2M1 && P <= 2 ? (NW >= 4 ? 4 : 3) : 1)))
 gemv_kernel(GemvArgs p) {
@@ -527,6 +529,9 @@ gemv_kernel(GemvArgs p) {
                 const float h1 = a[2] / (1.f + __expf(-a[2])) * a[3];
                 *reinterpret_cast<uint32_t *>(p.y + yrow * p.ldy + n0 / 2) =
                     bf16_bits(h0) | (bf16_bits(h1) << 16);
+            } else if (EPI) {
+                epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, yrow), a, n0, yrow, p.y,
+                          p.ldy);
             } else if (p.ws) {
                 *reinterpret_cast<v4f *>(p.ws + yrow * p.N + n0) = a;
             } else {
@@ -575,6 +580,9 @@ gemv_kernel(GemvArgs p) {
                         const float h1 = a[2] / (1.f + __expf(-a[2])) * a[3];
                         *reinterpret_cast<uint32_t *>(p.y + yrow * p.ldy + n0 / 2) =
                             bf16_bits(h0) | (bf16_bits(h1) << 16);
+                    } else if (EPI) {
+                        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, yrow), a, n0, yrow,
+                                  p.y, p.ldy);
                     } else if (p.ws) {
                         *reinterpret_cast<v4f *>(p.ws + yrow * p.N + n0) = a;
                     } else {
@@ -594,6 +602,7 @@ gemv_kernel(GemvArgs p) {
     }
 }
 
+#ifndef MX_WITH_EPILOGUE
 // Deterministic top-k combine: y[t][n] = sum_k w[t][k] * ys[t*topk + k][n],
 // k ascending, fp32, one bf16 rounding.  A thread owns 4 consecutive outputs
 // (N % 16 == 0) and issues the loads of 8 slots before summing them in order.
@@ -629,9 +638,9 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(int64_t T, int64_t top
 template <int ELEM, int LAYOUT, int ACT, bool MOE, int NW, int G>
 static hipError_t launch_p(const GemvArgs &a, int chunk, dim3 grid, hipStream_t st) {
     switch (chunk) {
-    case 2: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 2, G>), grid, dim3(NW * 64), 0, st, a); break;
-    case 4: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 4, G>), grid, dim3(NW * 64), 0, st, a); break;
-    default: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 8, G>), grid, dim3(NW * 64), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 2, G, false>), grid, dim3(NW * 64), 0, st, a); break;
+    case 4: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 4, G, false>), grid, dim3(NW * 64), 0, st, a); break;
+    default: hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, MOE, NW, 8, G, false>), grid, dim3(NW * 64), 0, st, a); break;
     }
     return hipGetLastError();
 }
@@ -663,6 +672,9 @@ static hipError_t launch_g(const GemvArgs &a, const GemvShape &sh, hipStream_t s
 
 hipError_t launch_gemv(int elem, int layout, int act, bool moe, const GemvArgs &a,
                        const GemvShape &sh, hipStream_t st) {
+    if (a.fin.on)
+        return moe ? hipErrorInvalidValue
+                   : launch_gemv_epi(elem, layout, act, a, (a.K + 127) / 128, st);
 #define MX_GEMV_CASE(EL, LA, AC, MO)                                                     \
     if (elem == EL && layout == LA && act == AC && moe == MO)                              \
         return launch_g<EL, LA, AC, MO>(a, sh, st);
@@ -684,5 +696,49 @@ hipError_t launch_moe_combine(int64_t T, int64_t topk, int64_t N, const float *y
                        topk, N, ys, wts, (uint16_t *)y);
     return hipGetLastError();
 }
+
+#else  // MX_WITH_EPILOGUE
+
+template <int ELEM, int LAYOUT, int ACT>
+static hipError_t launch_steps(const GemvArgs &a, int64_t steps, hipStream_t st) {
+    const int64_t T = a.N / 16;
+    const unsigned batches = (unsigned)((a.rows + 15) / 16);
+    const dim3 one((unsigned)T, batches), two((unsigned)((T + 1) / 2), batches);
+    // (MXFP8 activations come here with more than 64 steps only)
+    if (ACT == ACT_MXFP8 || steps >= 32) {
+        hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 2, true>), two, dim3(512), 0,
+                           st, a);
+    } else if constexpr (ACT != ACT_MXFP8) {
+        if (steps >= 16)
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 4, 4, 1, true>), one, dim3(256), 0,
+                               st, a);
+        else if (steps >= 8)
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 2, 8, 1, true>), one, dim3(128), 0,
+                               st, a);
+        else if (steps >= 2)
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 2, 2, 1, true>), one, dim3(128), 0,
+                               st, a);
+        else
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 1, 2, 1, true>), one, dim3(64), 0,
+                               st, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, int64_t steps,
+                           hipStream_t st) {
+    if (elem == E2M1 && layout == ROW32 && act == ACT_BF16)
+        return launch_steps<E2M1, ROW32, ACT_BF16>(a, steps, st);
+    if (elem != E4M3) return hipErrorInvalidValue;
+    if (act == ACT_MXFP8)
+        return layout == ROW32 ? launch_steps<E4M3, ROW32, ACT_MXFP8>(a, steps, st)
+                               : launch_steps<E4M3, BLK32, ACT_MXFP8>(a, steps, st);
+    if (act == ACT_BF16)
+        return layout == ROW32 ? launch_steps<E4M3, ROW32, ACT_BF16>(a, steps, st)
+                               : launch_steps<E4M3, BLK32, ACT_BF16>(a, steps, st);
+    return hipErrorInvalidValue;
+}
+
+#endif
 
 }  // namespace mx

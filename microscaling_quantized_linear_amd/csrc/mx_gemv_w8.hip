@@ -29,11 +29,25 @@
 // does not depend on timing), then the bias is added and y rounded to bf16
 // once.
 #include "mx_device.h"
+#include "mx_epilogue.h"
 #include "mx_kernels.h"
 
 #include <type_traits>
 
+// mx_gemv_w8_epi.hip compiles these kernels again with an epilogue
+#ifdef MX_WITH_EPILOGUE
+#define MX_LAUNCH(name) name##_epi
+#else
+#define MX_LAUNCH(name) name
+#endif
+
 namespace mx {
+
+#ifdef MX_WITH_EPILOGUE
+constexpr bool kEpi = true;
+#else
+constexpr bool kEpi = false;
+#endif
 
 typedef __attribute__((address_space(3))) void lds_void_w8;
 
@@ -48,7 +62,7 @@ __device__ inline void static_for(F &&f) {
 
 // XFRAG: activations in fragment order (xf, xct); else row-major (xq, xc).
 // G tiles per workgroup, SPW = the most steps one wavefront owns.
-template <int LAYOUT, bool XFRAG, int G, int SPW>
+template <int LAYOUT, bool XFRAG, int G, int SPW, bool EPI>
 __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
     constexpr int NQ = (SPW + 6) / 4;                   // quads SPW steps can span
     __shared__ __attribute__((aligned(1024))) uint8_t xs[8][SPW * 2048];
@@ -209,6 +223,10 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
         if (!live) continue;
         // lane (r, j) holds rows 4 j .. 4 j + 3 of the tile for token r
         const int64_t n0 = 16 * (t0 + g) + 4 * j;
+        if constexpr (EPI) {
+            epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+            continue;
+        }
         float v[4] = {a[0], a[1], a[2], a[3]};
         if (p.bias)
             for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.bias[n0 + e]);
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
 // activation copies and both codes follow, then the remaining weight chunks.
 // Measured on MI355X, every cycle between the start of a wavefront and its
 // weight requests adds to the time of this HBM-bound kernel.
-template <int LAYOUT, int G, int SPW, int NW>
+template <int LAYOUT, int G, int SPW, int NW, bool EPI>
 __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
     constexpr int NQ = (SPW + 6) / 4;                   // quads SPW steps can span
     static_assert(2 * G * (SPW - 1) < 64, "vmcnt holds 6 bits");
@@ -353,6 +371,10 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
     if (row >= p.M) return;
     // lane (r, j) holds rows 4 j .. 4 j + 3 of the tile for token r
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
+    if constexpr (EPI) {
+        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        return;
+    }
     float v[4] = {a[0], a[1], a[2], a[3]};
     if (p.bias)
         for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.bias[n0 + e]);
@@ -399,7 +421,7 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
 // slower.  Results are
 // identical to mx_quant_act_t16 followed by the even-shape kernel: the same
 // bytes, codes and MFMA order.
-template <int LAYOUT, int RULE, int G, int SPW, int NW, bool FULL>
+template <int LAYOUT, int RULE, int G, int SPW, int NW, bool FULL, bool EPI>
 __global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
     constexpr int XA = SPW > 4 ? 4 : SPW;              // steps of activations requested first
     constexpr int WIN = 1;                             // steps of weight chunks in flight
@@ -665,6 +687,10 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
 #pragma unroll
     for (int w2 = 1; w2 < NW; ++w2) a += red[w2][g][lane];
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
+    if constexpr (EPI) {
+        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        return;
+    }
     float v[4] = {a[0], a[1], a[2], a[3]};
     if (p.bias)
         for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.bias[n0 + e]);
@@ -686,7 +712,7 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
 // byte is token r's code of block 4 s + j, read from the row-major codes.
 // Weight chunks as in the T16 kernel.  The product is the T16 path's, bit for
 // bit (same bytes, codes and MFMA order).
-template <int LAYOUT, int G, int SPW, int NW>
+template <int LAYOUT, int G, int SPW, int NW, bool EPI>
 __global__ void __launch_bounds__(NW * 64) gemv_w8_rm_kernel(GemvW8Args p) {
     static_assert(2 * G * (SPW - 1) < 64, "vmcnt holds 6 bits");
     __shared__ __attribute__((aligned(1024))) uint8_t xs[NW][SPW * 2048];
@@ -821,6 +847,10 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_rm_kernel(GemvW8Args p) {
 #pragma unroll
     for (int w2 = 1; w2 < NW; ++w2) a += red[w2][g][lane];
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
+    if constexpr (EPI) {
+        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        return;
+    }
     float v[4] = {a[0], a[1], a[2], a[3]};
     if (p.bias)
         for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.bias[n0 + e]);
@@ -864,21 +894,22 @@ static hipError_t launch_fused(int layout, int rule, const GemvW8Args &a, const 
         constexpr int G = decltype(gc)::value, SPW = decltype(sc)::value;
         if (layout == ROW32) {
             if (rule == RULE_OCP)
-                hipLaunchKernelGGL((gemv_w8_fused_kernel<ROW32, RULE_OCP, G, SPW, 8, FULL>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_fused_kernel<ROW32, RULE_OCP, G, SPW, 8, FULL, kEpi>), grid, block, 0, st, a);
             else
-                hipLaunchKernelGGL((gemv_w8_fused_kernel<ROW32, RULE_CEIL448, G, SPW, 8, FULL>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_fused_kernel<ROW32, RULE_CEIL448, G, SPW, 8, FULL, kEpi>), grid, block, 0, st, a);
         } else {
             if (rule == RULE_OCP)
-                hipLaunchKernelGGL((gemv_w8_fused_kernel<BLK32, RULE_OCP, G, SPW, 8, FULL>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_fused_kernel<BLK32, RULE_OCP, G, SPW, 8, FULL, kEpi>), grid, block, 0, st, a);
             else
-                hipLaunchKernelGGL((gemv_w8_fused_kernel<BLK32, RULE_CEIL448, G, SPW, 8, FULL>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_fused_kernel<BLK32, RULE_CEIL448, G, SPW, 8, FULL, kEpi>), grid, block, 0, st, a);
         }
         return hipSuccess;
     });
 }
 
-hipError_t launch_gemv_w8_fused(int layout, int rule, const GemvW8Args &a, const GemvW8Plan &pl,
-                                hipStream_t st) {
+hipError_t MX_LAUNCH(launch_gemv_w8_fused)(int layout, int rule, const GemvW8Args &a,
+                                           const GemvW8Plan &pl, hipStream_t st) {
+    if (!kEpi && a.fin.on) return launch_gemv_w8_fused_epi(layout, rule, a, pl, st);
     if (!gemv_w8_even(a.N, a.K, pl) || a.K % 128 != 0) return hipErrorInvalidValue;
     const hipError_t e = a.M % 16 == 0 ? launch_fused<true>(layout, rule, a, pl, st)
                                        : launch_fused<false>(layout, rule, a, pl, st);
@@ -891,19 +922,19 @@ static hipError_t launch_w8_spw(const GemvW8Args &a, const GemvW8Plan &pl, hipSt
     const dim3 grid((unsigned)((a.N / 16 + G - 1) / G), (unsigned)((a.M + 15) / 16));
     const dim3 block((unsigned)(pl.nw * 64));
     switch (pl.spw) {
-    case 1: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 1>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 2>), grid, block, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 4>), grid, block, 0, st, a); break;
+    case 1: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 1, kEpi>), grid, block, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 2, kEpi>), grid, block, 0, st, a); break;
+    case 4: hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 4, kEpi>), grid, block, 0, st, a); break;
     case 7:
         if constexpr (G * 7 <= 16)
-            hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 7>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 7, kEpi>), grid, block, 0, st, a);
         else
             return hipErrorInvalidValue;
         break;
     default:
         // the plan keeps G * SPW <= 16 (registers)
         if constexpr (G * 8 <= 16)
-            hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 8>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((gemv_w8_kernel<LAYOUT, XFRAG, G, 8, kEpi>), grid, block, 0, st, a);
         else
             return hipErrorInvalidValue;
         break;
@@ -920,16 +951,17 @@ static hipError_t launch_w8_g(const GemvW8Args &a, const GemvW8Plan &pl, hipStre
     }
 }
 
-hipError_t launch_gemv_w8(int layout, bool xfrag, const GemvW8Args &a, const GemvW8Plan &pl,
-                          hipStream_t st) {
+hipError_t MX_LAUNCH(launch_gemv_w8)(int layout, bool xfrag, const GemvW8Args &a,
+                                     const GemvW8Plan &pl, hipStream_t st) {
+    if (!kEpi && a.fin.on) return launch_gemv_w8_epi(layout, xfrag, a, pl, st);
     if (xfrag && gemv_w8_even(a.N, a.K, pl)) {
         const dim3 grid((unsigned)(a.N / 16 / pl.g), (unsigned)((a.M + 15) / 16)), block(512);
         const hipError_t e = even_dispatch(pl, [&](auto gc, auto sc) -> hipError_t {
             constexpr int G = decltype(gc)::value, SPW = decltype(sc)::value;
             if (layout == ROW32)
-                hipLaunchKernelGGL((gemv_w8_even_kernel<ROW32, G, SPW, 8>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_even_kernel<ROW32, G, SPW, 8, kEpi>), grid, block, 0, st, a);
             else
-                hipLaunchKernelGGL((gemv_w8_even_kernel<BLK32, G, SPW, 8>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_even_kernel<BLK32, G, SPW, 8, kEpi>), grid, block, 0, st, a);
             return hipSuccess;
         });
         if (e != hipSuccess) return e;
@@ -940,9 +972,9 @@ hipError_t launch_gemv_w8(int layout, bool xfrag, const GemvW8Args &a, const Gem
         const hipError_t e = even_dispatch(pl, [&](auto gc, auto sc) -> hipError_t {
             constexpr int G = decltype(gc)::value, SPW = decltype(sc)::value;
             if (layout == ROW32)
-                hipLaunchKernelGGL((gemv_w8_rm_kernel<ROW32, G, SPW, 8>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_rm_kernel<ROW32, G, SPW, 8, kEpi>), grid, block, 0, st, a);
             else
-                hipLaunchKernelGGL((gemv_w8_rm_kernel<BLK32, G, SPW, 8>), grid, block, 0, st, a);
+                hipLaunchKernelGGL((gemv_w8_rm_kernel<BLK32, G, SPW, 8, kEpi>), grid, block, 0, st, a);
             return hipSuccess;
         });
         if (e != hipSuccess) return e;

@@ -12,8 +12,20 @@ enum { E4M3 = 0, E2M1 = 1 };
 enum { ROW32 = 0, BLK32 = 1 };
 enum { RULE_OCP = 0, RULE_CEIL448 = 1 };
 enum { ACT_BF16 = 0, ACT_MXFP8 = 1, ACT_MXFP8_T16 = 2 };
+enum { FLOAT_BF16 = 0, FLOAT_F32 = 1 };
+enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
 
 constexpr int kMoeMaxPairs = 4096;   // T * topk handled by one routing scan
+
+// What a dense product does behind its bias (mx_epilogue.h): y = f(z) (+ residual),
+// or, gated, f(z[2 n]) * z[2 n + 1] (+ residual) in N / 2 columns.
+enum { FN_NONE = 0, FN_RELU = 1, FN_RELU2 = 2, FN_SILU = 3, FN_GELU = 4, FN_GELU_TANH = 5 };
+struct EpiArgs {
+    int on;                  // 0: none of it (the kernels without an epilogue run)
+    int fn, gated;
+    const uint16_t *res;     // bf16 [M, ldr] or null
+    int64_t ldr;
+};
 
 struct GemvArgs {
     const uint8_t *w;        // packed W-T16 weights (all experts)
@@ -33,6 +45,7 @@ struct GemvArgs {
     float *ws;               // MoE combine mode: fp32 per-slot rows [T*topk, N]
     int xslot;               // MoE: activation row of pair i is i (else i / topk)
     int epi;                 // MoE: 1 = silu(row 2i) * row 2i+1 -> output i (width N / 2)
+    EpiArgs fin;             // dense only
 };
 
 struct GemmArgs {
@@ -43,6 +56,7 @@ struct GemmArgs {
     const uint16_t *bias;
     uint16_t *y;
     int64_t ldy;
+    EpiArgs fin;
 };
 
 // bytes of the XC-T16 activation-code staging for M rows
@@ -105,6 +119,11 @@ hipError_t launch_gemv(int elem, int layout, int act, bool moe, const GemvArgs &
 hipError_t launch_moe_combine(int64_t T, int64_t topk, int64_t N, const float *ys,
                               const float *wts, void *y, hipStream_t stream);
 hipError_t launch_gemm(int layout, const GemmArgs &a, hipStream_t stream);
+// the launchers above and those of the W8A8 GEMV hand calls with an epilogue
+// (fin.on) to these, whose kernels hold one
+hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, int64_t steps,
+                           hipStream_t stream);
+hipError_t launch_gemm_epi(int layout, const GemmArgs &a, hipStream_t stream);
 int gemm_tile_n(int64_t N);
 
 // W8A8 decode GEMV (mx_gemv_w8.hip).  Activations either row-major (xq
@@ -122,6 +141,7 @@ struct GemvW8Args {
     const uint16_t *bias;
     uint16_t *y;
     int64_t ldy;
+    EpiArgs fin;
 };
 // nw wavefronts per workgroup, each with at most spw steps; g tiles per
 // workgroup; ok = false if the steps do not fit the register plan
@@ -132,6 +152,8 @@ struct GemvW8Plan {
 GemvW8Plan plan_gemv_w8(int64_t T, int64_t S, int64_t MB, int nw_force, int g_force);
 hipError_t launch_gemv_w8(int layout, bool xt16, const GemvW8Args &a, const GemvW8Plan &plan,
                           hipStream_t stream);
+hipError_t launch_gemv_w8_epi(int layout, bool xt16, const GemvW8Args &a, const GemvW8Plan &plan,
+                              hipStream_t stream);
 // True when the plan divides the shape evenly: eight wavefronts of exactly
 // `spw` steps, whole tiles per workgroup.  Then T16 input runs the even-shape
 // kernel, and bf16 input with K % 128 == 0 can be quantized inside the GEMV.
@@ -140,6 +162,8 @@ bool gemv_w8_even(int64_t N, int64_t K, const GemvW8Plan &plan);
 // in mx_quant_act); requires gemv_w8_even and K % 128 == 0.
 hipError_t launch_gemv_w8_fused(int layout, int rule, const GemvW8Args &a,
                                 const GemvW8Plan &plan, hipStream_t stream);
+hipError_t launch_gemv_w8_fused_epi(int layout, int rule, const GemvW8Args &a,
+                                    const GemvW8Plan &plan, hipStream_t stream);
 
 // per-token quantization into the T16 layout (mx_quant.hip)
 hipError_t launch_quant_t16(int64_t M, int64_t K, const void *x, int64_t ldx, void *xq,
@@ -239,5 +263,52 @@ constexpr int64_t kLoraMaxK = int64_t(1) << 26;
 constexpr int64_t kCombineMaxCols = 65535 * 2048;
 int64_t lora_splits(int64_t M, int64_t K, bool invariant);
 hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
+
+// ---- between the products of a layer (mx_layer_api.cpp) ----
+
+// The choice of experts (mx_router.hip).
+struct RouteArgs {
+    int64_t T;
+    int E, topk;
+    const void *logits;            // fp32 or bf16 [T, ldl]
+    int64_t ldl;
+    const float *bias;             // [E] or null
+    int score;
+    int groups, per_group, topk_groups, group_best;
+    int group_mul;                 // e / per_group = e * group_mul >> 20 for e < 1024
+    int renorm;
+    float scale;
+    int32_t *ids;                  // [T, topk]
+    float *weights;
+};
+constexpr int64_t kRouteMaxExperts = 1024;     // a choice's number holds ten bits of expert
+constexpr int kRouteMaxGroups = 64, kRouteMaxTopk = 64;
+hipError_t launch_moe_route(const RouteArgs &a, int type, hipStream_t stream);
+
+// The norms around a block with its gate and residual scale (mx_block.hip).
+struct BlockNormArgs {
+    int64_t M, K;
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *post;          // weight of the norm behind the block, or null: no norm
+    const uint16_t *gate;          // [gates, ldg] or null: 1
+    int64_t gates, ldg;
+    const int32_t *gate_ids;       // [M] or null: row 0
+    const void *res;               // bf16 or fp32 [M, ldr] or null: 0
+    int64_t ldr;
+    float alpha;
+    const uint16_t *weight;        // of the norm ahead of the next block, or null: none
+    float offset, eps;
+    void *sum;                     // the residual's type [M, lds] or null
+    int64_t lds;
+    uint16_t *y;
+    int64_t ldy;
+    uint8_t *xq;
+    int64_t ldq;
+    uint8_t *xcodes;
+    int64_t ldc;
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, int stream_type, int act, int rule,
+                             hipStream_t stream);
 
 }  // namespace mx
