@@ -30,11 +30,10 @@ def _sum32(*v):
 def route(x, score, bias, groups, topk_groups, group_best, topk, renorm, scale):
     """(ids, weights, bound) of logits x (float32 or float64 [T, E]); bias float32.
 
-    Bound of a weight, relative: with s formed in 64 bits and rounded once, s is off
-    by half a step; in fp32 the exponential is off by a last place (two half steps)
-    and its rounded argument adds |x - max| of them, the sum by as much and by at
-    most ten additions, a division by one.  Over their sum: topk additions and a
-    division; the scale one more."""
+    Bound of a weight, relative, in half steps of fp32: the exponential is off by a
+    last place (two) and its rounded argument adds |x - max|, the sum by as much and
+    by at most ten additions, its reciprocal and a product two.  Over their sum: topk
+    additions and a division, of values that far off; the scale one more."""
     x = np.asarray(x, np.float64)
     T, E = x.shape
     with np.errstate(invalid="ignore"):
@@ -50,15 +49,14 @@ def route(x, score, bias, groups, topk_groups, group_best, topk, renorm, scale):
             total = e.sum(1, keepdims=True)
             s = np.where(total > 0, e / np.where(total > 0, total, 1), 0.0)
     depth = np.where(masked, 0.0, np.minimum(top - x, 104.0)).max(1) if score == SOFTMAX else 0.0
+    tol = 20 + 2 * depth + 2 * topk
     if bias is None:
         c = x
-        tol = 20 + 2 * depth + 2 * topk
     else:
         b = bias.astype(np.float32)
         masked = masked | ~(b > -np.inf)[None]
         c = np.minimum(_sum32(s.astype(np.float32), np.broadcast_to(b, (T, E))), np.float32(MOST))
         c = np.where(masked, -np.inf, c.astype(np.float64))
-        tol = 0 * depth + 4 + 2 * topk
     if groups > 1:
         by = np.sort(c.reshape(T, groups, -1), axis=2)[:, :, ::-1]
         near = by[:, :, 0] if group_best == 1 else \
