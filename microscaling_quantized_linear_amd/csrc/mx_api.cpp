@@ -542,7 +542,8 @@ static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const vo
         g.ldy = ldy;
         g.fin = fin;
         log_dispatch("linear: gemm_w8a8_kernel %s%s, %d x 256 tiles; M=%lld N=%lld K=%lld",
-                     layout_name(layout), with, mx::gemm_tile_n(N), (long long)M, (long long)N,
+                     layout_name(layout), with,
+                     fin.on ? mx::gemm_epi_tile_n(M, N) : mx::gemm_tile_n(N), (long long)M, (long long)N,
                      (long long)K);
         return launched(mx::launch_gemm(layout, g, s));
     }

@@ -229,9 +229,17 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
     // step, eight steps an iteration, so the phase repeats).
     constexpr int kMem = NTW + 8;                         // memory ops per step
     constexpr int NG = 2 * NTW;                           // groups (kh, nt), kh major
-    // the group that issues memory op e: activations 0..7 in groups 0..7,
-    // the copies in the last NTW groups
-    auto op_group = [](int e) { return e < 8 ? e : e - 8 + (NG - NTW); };
+    // the group that issues memory op e: activations 0..7 in groups 0..7 (two a group
+    // where there are four), the copies in the last NTW groups
+    constexpr auto op_group = [](int e) constexpr {
+        return e < 8 ? (NG >= 8 ? e : e / 2) : e - 8 + (NG - NTW);
+    };
+    // those out before the barrier
+    constexpr int kBefore = [=] {
+        int n = 0;
+        for (int e = 0; e < kMem; ++e) n += op_group(e) <= NG - 2 ? 1 : 0;
+        return n;
+    }();
     static_assert(NG - NTW <= 8 && NTW >= 2, "schedule fits the step");
     static_assert((8 * NG) % 4 == 0, "ring phase repeats every iteration");
     v8i af[4];
@@ -254,11 +262,10 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
             if (k == NG - 2) {
                 // this wavefront's copies of step s + 1 (issued during step
                 // s - 1, before all of this step's loads) have landed; of this
-                // step's loads, those of groups 0 .. NG - 2 are out: all but
-                // the last copy
-                static_assert(op_group(kMem - 2) <= NG - 2 && op_group(kMem - 1) == NG - 1,
-                              "kMem - 1 loads before the barrier");
-                __builtin_amdgcn_s_waitcnt(vmcnt_only(kMem - 1));
+                // step's loads, those of groups 0 .. NG - 2 are out (of seven and
+                // eight tiles all but the last copy)
+                static_assert(NG < 14 || kBefore == kMem - 1, "kMem - 1 loads before the barrier");
+                __builtin_amdgcn_s_waitcnt(vmcnt_only(kBefore));
                 step_barrier();
             }
             if (k + 2 < NG) issue(cur, k + 2, (PH + k + 2) % 4);
@@ -588,7 +595,13 @@ int gemm_tile_n(int64_t N) {
 
 hipError_t MX_LAUNCH(launch_gemm)(int layout, const GemmArgs &a, hipStream_t st) {
     if (!kEpi && a.fin.on) return launch_gemm_epi(layout, a, st);
+#ifdef MX_WITH_EPILOGUE
+    const int bn = gemm_epi_tile_n(a.M, a.N);
+    if (bn == 64) return layout == ROW32 ? launch_ntw<ROW32, 2>(a, st) : launch_ntw<BLK32, 2>(a, st);
+    if (bn == 128) return layout == ROW32 ? launch_ntw<ROW32, 4>(a, st) : launch_ntw<BLK32, 4>(a, st);
+#else
     const int bn = gemm_tile_n(a.N);
+#endif
     if (layout == ROW32)
         return bn == 224 ? launch_ntw<ROW32, 7>(a, st) : launch_ntw<ROW32, 8>(a, st);
     return bn == 224 ? launch_ntw<BLK32, 7>(a, st) : launch_ntw<BLK32, 8>(a, st);

@@ -125,6 +125,7 @@ hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, int
                            hipStream_t stream);
 hipError_t launch_gemm_epi(int layout, const GemmArgs &a, hipStream_t stream);
 int gemm_tile_n(int64_t N);
+int gemm_epi_tile_n(int64_t M, int64_t N);   // with an epilogue (mx_plan.cpp)
 
 // W8A8 decode GEMV (mx_gemv_w8.hip).  Activations either row-major (xq
 // [M, ldq], codes xc [M, ldc]) or in the T16 layout (xf, xct; mx_quant.hip).

@@ -11,6 +11,21 @@ bool gemv_w8_even(int64_t N, int64_t K, const GemvW8Plan &pl) {
            pl.g * pl.spw <= 16;
 }
 
+// Weight rows of a tile of the prefill GEMM with an epilogue: the fewest, 64 or 128, at
+// which every tile of 256 tokens has a compute unit of its own; from more than 256
+// tiles of 128 rows on, those of mx_linear (224 or 256).  A tile's time is its
+// products, a step of 128 K at 0.92 us for 256 rows, and its epilogue, one wavefront a
+// SIMD: with idle compute units both shrink with the tile.  Measured, us at 256 / 128 /
+// 64 rows (K 1568, GELU and residual): M 512, N 2048 28.8 / 16.4 / 10.6; M 1001, N 4096
+// 30.3 / 17.8 / 13.2; M 2048, N 4096 33.6 / 23.6 / 23.7; M 3000, N 4096 36.8 / 37.0 /
+// 34.5; M 4096, N 7168 66.9 / 76.6 / 71.7 (K 7168: 170 / 197 / 213).
+int gemm_epi_tile_n(int64_t M, int64_t N) {
+    const int64_t mt = (M + 255) / 256;
+    for (int bn : {64, 128})
+        if ((N + bn - 1) / bn * mt <= 256) return bn;
+    return gemm_tile_n(N);
+}
+
 // Launch plan for T tiles, S steps and MB 16-token grid rows: tiles per
 // workgroup G in {4, 2, 1} (the largest that still gives about one
 // workgroup per compute unit, measured best on MI355X), up to eight

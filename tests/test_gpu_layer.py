@@ -474,7 +474,10 @@ LINEAR = [  # elem, layout, M, N, K, act, form
     # prefill
     (0, 0, 65, 16, 32, MXFP8, "x"), (0, 1, 130, 288, 544, MXFP8, "x"), (0, 0, 300, 272, 1024, MXFP8, "given"),
     (0, 1, 257, 1792, 640, MXFP8, "t16"), (0, 0, 100, 1792, 1568, MXFP8, "x"),
-    (0, 1, 70, 320, 2208, MXFP8, "t16"), (0, 0, 513, 240, 96, MXFP8, "x"), (0, 0, 66, 3584, 384, MXFP8, "x")]
+    (0, 1, 70, 320, 2208, MXFP8, "t16"), (0, 0, 513, 240, 96, MXFP8, "x"), (0, 0, 66, 3584, 384, MXFP8, "x"),
+    # more than a tile of 64 or of 128 weight rows for each compute unit
+    (0, 0, 1025, 3600, 160, MXFP8, "t16"), (0, 1, 2100, 3616, 1056, MXFP8, "x"),
+    (0, 0, 1800, 5376, 160, MXFP8, "x"), (0, 1, 2500, 4064, 1184, MXFP8, "given")]
 
 
 @pytest.mark.parametrize("elem,layout,M,N,K,act,form", LINEAR)
