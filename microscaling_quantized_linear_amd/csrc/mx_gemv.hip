@@ -322,6 +322,16 @@ gemv_kernel(GemvArgs p) {
         const uint32_t xbase = live ? (uint32_t)(xrow * p.ldx * xelt) : 0u;
         const uint32_t cxbase = live ? (uint32_t)(xrow * p.ldc) : 0u;
 
+        // what the epilogue reads for the tile that this wavefront finishes, ahead of
+        // the products: it is not waited for then
+        static_assert(!EPI || G <= NW, "one tile a wavefront");
+        EpiLane el;
+        if constexpr (EPI) {
+            if (wave < ntiles && live)
+                el = epi_load(p.fin, p.bias, 16 * (t0 + wave) + 4 * j, yrow);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+
         v4f acc[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) acc[g] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -530,8 +540,7 @@ gemv_kernel(GemvArgs p) {
                 *reinterpret_cast<uint32_t *>(p.y + yrow * p.ldy + n0 / 2) =
                     bf16_bits(h0) | (bf16_bits(h1) << 16);
             } else if (EPI) {
-                epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, yrow), a, n0, yrow, p.y,
-                          p.ldy);
+                epi_store(p.fin, p.bias, el, a, n0, yrow, p.y, p.ldy);
             } else if (p.ws) {
                 *reinterpret_cast<v4f *>(p.ws + yrow * p.N + n0) = a;
             } else {
@@ -581,8 +590,7 @@ gemv_kernel(GemvArgs p) {
                         *reinterpret_cast<uint32_t *>(p.y + yrow * p.ldy + n0 / 2) =
                             bf16_bits(h0) | (bf16_bits(h1) << 16);
                     } else if (EPI) {
-                        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, yrow), a, n0, yrow,
-                                  p.y, p.ldy);
+                        epi_store(p.fin, p.bias, el, a, n0, yrow, p.y, p.ldy);
                     } else if (p.ws) {
                         *reinterpret_cast<v4f *>(p.ws + yrow * p.N + n0) = a;
                     } else {
@@ -706,8 +714,15 @@ static hipError_t launch_steps(const GemvArgs &a, int64_t steps, hipStream_t st)
     const dim3 one((unsigned)T, batches), two((unsigned)((T + 1) / 2), batches);
     // (MXFP8 activations come here with more than 64 steps only)
     if (ACT == ACT_MXFP8 || steps >= 32) {
-        hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 2, true>), two, dim3(512), 0,
-                           st, a);
+        // one tile a workgroup while every tile has a compute unit of its own (N 4096, K
+        // 7168: e4m3 11.2 -> 8.8 us, e2m1 8.5 -> 7.4); else two, which share the
+        // activations (N 7168, K 4096: 8.6 against 10.6, e2m1 6.5 against 8.8)
+        if (T * batches <= 256)
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 1, true>), one, dim3(512),
+                               0, st, a);
+        else
+            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 2, true>), two, dim3(512),
+                               0, st, a);
     } else if constexpr (ACT != ACT_MXFP8) {
         if (steps >= 16)
             hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 4, 4, 1, true>), one, dim3(256), 0,

@@ -81,6 +81,16 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
     const int n = (int)(s1 - s0);                       // <= SPW (host plan)
     const int64_t qa = s0 / 4;                          // first quad of the range
 
+    // what the epilogue reads, ahead of everything: it is not waited for then
+    EpiLane el[EPI ? G : 1];
+    if constexpr (EPI) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            if (g * nw + wave < ntiles && live)
+                el[g] = epi_load(p.fin, p.bias, 16 * (t0 + g * nw + wave) + 4 * j, row);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
     // ---- 1. activation fragments of steps s0 .. s1 - 1 -> LDS ----
     uint8_t *myx = xs[wave];
     const __amdgpu_buffer_rsrc_t xr =
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
         // lane (r, j) holds rows 4 j .. 4 j + 3 of the tile for token r
         const int64_t n0 = 16 * (t0 + g) + 4 * j;
         if constexpr (EPI) {
-            epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+            epi_store(p.fin, p.bias, el[g / nw], a, n0, row, p.y, p.ldy);
             continue;
         }
         float v[4] = {a[0], a[1], a[2], a[3]};
@@ -261,6 +271,15 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
     const uint32_t t0 = blockIdx.x * G;
     const uint32_t s0 = wave * SPW, qa = s0 / 4;
     const uint32_t lo = 16 * lane;
+
+    // what the epilogue reads, ahead of everything: it is not waited for then
+    EpiLane el;
+    if constexpr (EPI) {
+        const int64_t row = 16 * (int64_t)mb + r;
+        if (wave < G && row < p.M)
+            el = epi_load(p.fin, p.bias, 16 * (int64_t)(t0 + wave) + 4 * j, row);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
     // ---- 1. the first step's weight chunks ----
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.w + (size_t)t0 * S * 2048, G * S * 2048);
@@ -372,7 +391,7 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
     // lane (r, j) holds rows 4 j .. 4 j + 3 of the tile for token r
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
     if constexpr (EPI) {
-        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        epi_store(p.fin, p.bias, el, a, n0, row, p.y, p.ldy);
         return;
     }
     float v[4] = {a[0], a[1], a[2], a[3]};
@@ -440,6 +459,15 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
     const uint32_t t0 = blockIdx.x * G;
     const uint32_t s0 = wave * SPW;
     const uint32_t lo = 16 * lane;
+
+    // what the epilogue reads, ahead of everything: it is not waited for then
+    EpiLane el;
+    if constexpr (EPI) {
+        const int64_t row = 16 * (int64_t)mb + r;
+        if (wave < G && row < p.M)
+            el = epi_load(p.fin, p.bias, 16 * (int64_t)(t0 + wave) + 4 * j, row);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
     // ---- 1. raw bf16 activations of the wavefront's steps ----
     // load u of a step: token 16 mb + 4 u + j, bytes 16 r of the step's 256;
@@ -688,7 +716,7 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
     for (int w2 = 1; w2 < NW; ++w2) a += red[w2][g][lane];
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
     if constexpr (EPI) {
-        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        epi_store(p.fin, p.bias, el, a, n0, row, p.y, p.ldy);
         return;
     }
     float v[4] = {a[0], a[1], a[2], a[3]};
@@ -726,6 +754,15 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_rm_kernel(GemvW8Args p) {
     const uint32_t t0 = blockIdx.x * G;
     const uint32_t s0 = wave * SPW;
     const uint32_t lo = 16 * lane;
+
+    // what the epilogue reads, ahead of everything: it is not waited for then
+    EpiLane el;
+    if constexpr (EPI) {
+        const int64_t row = 16 * (int64_t)mb + r;
+        if (wave < G && row < p.M)
+            el = epi_load(p.fin, p.bias, 16 * (int64_t)(t0 + wave) + 4 * j, row);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
     // ---- 1. the first step's weight chunks ----
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.w + (size_t)t0 * S * 2048, G * S * 2048);
@@ -848,7 +885,7 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_rm_kernel(GemvW8Args p) {
     for (int w2 = 1; w2 < NW; ++w2) a += red[w2][g][lane];
     const int64_t n0 = 16 * (int64_t)(t0 + g) + 4 * j;
     if constexpr (EPI) {
-        epi_store(p.fin, p.bias, epi_load(p.fin, p.bias, n0, row), a, n0, row, p.y, p.ldy);
+        epi_store(p.fin, p.bias, el, a, n0, row, p.y, p.ldy);
         return;
     }
     float v[4] = {a[0], a[1], a[2], a[3]};
