@@ -308,8 +308,8 @@ struct BlockNormArgs {
     int64_t ldq;
     uint8_t *xcodes;
     int64_t ldc;
+    int rule;
 };
-hipError_t launch_block_norm(const BlockNormArgs &a, int stream_type, int act, int rule,
-                             hipStream_t stream);
+hipError_t launch_block_norm(const BlockNormArgs &a, int stream_type, int act, hipStream_t stream);
 
 }  // namespace mx

@@ -158,6 +158,7 @@ mx_status mx_block_norm(int64_t M, int64_t K, const void *x, int64_t ldx, const 
     a.ldq = ldq;
     a.xcodes = static_cast<uint8_t *>(xcodes);
     a.ldc = ldc;
+    a.rule = rule;
     log_dispatch("block_norm: block_norm_kernel,%s%s %s stream, %s output (rule %d); M=%lld K=%lld",
                  post_weight ? " post norm," : "", gate ? " gate," : "",
                  stream_type == FLOAT_F32 ? "fp32" : "bf16",
@@ -166,7 +167,7 @@ mx_status mx_block_norm(int64_t M, int64_t K, const void *x, int64_t ldx, const 
                  : act == ACT_MXFP8  ? "row-major MXFP8"
                                      : "T16",
                  rule, (long long)M, (long long)K);
-    return launched(launch_block_norm(a, stream_type, act, rule, hip(stream)));
+    return launched(launch_block_norm(a, stream_type, act, hip(stream)));
 }
 
 }  // extern "C"

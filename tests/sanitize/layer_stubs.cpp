@@ -15,7 +15,7 @@ hipError_t launch_moe_route(const RouteArgs &, int, hipStream_t) {
     ++mx_layer_launches;
     return hipSuccess;
 }
-hipError_t launch_block_norm(const BlockNormArgs &, int, int, int, hipStream_t) {
+hipError_t launch_block_norm(const BlockNormArgs &, int, int, hipStream_t) {
     ++mx_layer_launches;
     return hipSuccess;
 }
