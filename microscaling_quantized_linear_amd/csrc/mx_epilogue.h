@@ -15,8 +15,8 @@ namespace mx {
 // The activations by what they cost: none, relu and relu2 are comparisons and a
 // product; silu and tanh-gelu are z times a logistic function of an odd cubic
 // (0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))), so one form with two coefficients
-// serves both; erf-gelu has its own.
-enum { KIND_SIMPLE = 0, KIND_LOGISTIC = 1, KIND_ERF = 2 };
+// serves both; erf-gelu has its own.  (KIND_NONE: the prefill kernel's form for none.)
+enum { KIND_SIMPLE = 0, KIND_LOGISTIC = 1, KIND_ERF = 2, KIND_NONE = 3 };
 __host__ __device__ inline int fn_kind(int fn) {
     return fn == FN_GELU ? KIND_ERF : fn >= FN_SILU ? KIND_LOGISTIC : KIND_SIMPLE;
 }
@@ -58,6 +58,8 @@ __device__ inline float fn_value(float z, const FnCoef &c) {
         q = __builtin_fmaf(q, u, -1.1386800506109441e-4f);
         const float e = __builtin_amdgcn_exp2f(t * t * -0.72134752044448170f);
         return __builtin_fmaf(-t, q * e, z < 0.0f ? 0.0f : z);
+    } else if constexpr (KIND == KIND_NONE) {
+        return z;
     } else {
         const float r = c.relu && z < 0.0f ? 0.0f : z;
         return c.square ? r * r : r;

@@ -394,9 +394,13 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
     if constexpr (EPI) {
         // With an epilogue: the sums leave their registers the same way, through
         // f, the gate and the residual, whose 16-byte pieces are read in the layout
-        // of the stores (a slab ahead) and traded back by the same swaps.  Gated:
-        // rows 2 i and 2 i + 1 give column i, so dword 2 a + g of a slab's eight
-        // holds columns 4 a + 2 g, + 1.
+        // of the stores and traded back by the same swaps.  All of a lane's pieces are
+        // asked for first, into the registers that the products no longer need (M and K
+        // 4096, N 7168, with its quantization: 123.3 us; a slab ahead: 124.7).  No
+        // product runs beside this, so an instruction for every value is 0.4 us a
+        // workgroup: a call without an activation has its own form (120.9 us).  Gated:
+        // rows 2 i and 2 i + 1 give column i, so dword 2 a + g of a slab's eight holds
+        // columns 4 a + 2 g, + 1.
         const FnCoef fc = fn_coef(p.fin.fn);
         const uint32_t ldr2 = (uint32_t)p.fin.ldr * 2u;
         const __amdgpu_buffer_rsrc_t resr =
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
                 const int row = 32 * nt + 16 * pc;
                 return row < left ? base + (GATED ? row : 2 * row) : kOOB;
             };
-            v4u res[2][2][PC];
+            v4u res[NTW][2][PC];
             auto fetch = [&](v4u (&r)[2][PC], int nt) {
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
@@ -429,10 +433,10 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
                         r[mt][pc] = load16(resr, off | (off & kOOB));
                     }
             };
-            fetch(res[0], 0);
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt) fetch(res[nt], nt);
 #pragma unroll
             for (int nt = 0; nt < NTW; ++nt) {
-                if (nt + 1 < NTW) fetch(res[(nt + 1) % 2], nt + 1);
                 v2u bias2[4];
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
                     auto lo16 = [](uint32_t v) { return __uint_as_float(v << 16); };
                     auto hi16 = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
                     if constexpr (GATED) {
-                        const v4u r = res[nt % 2][mt][0];
+                        const v4u r = res[nt][mt][0];
                         const auto r02 = __builtin_amdgcn_permlane32_swap(r[0], r[1], false, false);
                         const auto r13 = __builtin_amdgcn_permlane32_swap(r[2], r[3], false, false);
                         const uint32_t rd[4] = {r02[0], r13[0], r02[1], r13[1]};
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
                     } else {
 #pragma unroll
                         for (int pc = 0; pc < 2; ++pc) {
-                            const v4u r = res[nt % 2][mt][pc];
+                            const v4u r = res[nt][mt][pc];
                             uint32_t o[2][2], rd[2][2];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -499,6 +503,7 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
                 __builtin_amdgcn_sched_barrier(0);        // one slab at a time, as below
             }
         };
+        using KN = std::integral_constant<int, KIND_NONE>;
         using K0 = std::integral_constant<int, KIND_SIMPLE>;
         using K1 = std::integral_constant<int, KIND_LOGISTIC>;
         using K2 = std::integral_constant<int, KIND_ERF>;
@@ -508,7 +513,8 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
             else if (kind == KIND_LOGISTIC) finish(K1{}, std::true_type{});
             else finish(K2{}, std::true_type{});
         } else {
-            if (kind == KIND_SIMPLE) finish(K0{}, std::false_type{});
+            if (p.fin.fn == FN_NONE) finish(KN{}, std::false_type{});
+            else if (kind == KIND_SIMPLE) finish(K0{}, std::false_type{});
             else if (kind == KIND_LOGISTIC) finish(K1{}, std::false_type{});
             else finish(K2{}, std::false_type{});
         }
