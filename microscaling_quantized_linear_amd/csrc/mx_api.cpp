@@ -462,8 +462,11 @@ static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const vo
             if (mx::overlap(sy, in) || mx::overlap(sw, in)) return MX_ERR_UNSUPPORTED;
         if (!mx::apart_or_same(sy, sr) || mx::overlap(sw, sr) || mx::overlap(sw, sy))
             return MX_ERR_UNSUPPORTED;
-        // without any of it the kernels of mx_linear run
-        fin.on = end->fn != mx::FN_NONE || end->gated || res;
+        // Without any of it the kernels of mx_linear run, but where the prefill's kernel
+        // with an epilogue has smaller tiles that leave no compute unit without one (M
+        // 1001, N 4096, K 1568: 11.3 against 23.4 us).
+        fin.on = end->fn != mx::FN_NONE || end->gated || res ||
+                 (gemm && mx::gemm_epi_tile_n(M, N) < mx::gemm_tile_n(N));
         fin.fn = end->fn;
         fin.gated = end->gated;
         fin.res = static_cast<const uint16_t *>(res);
