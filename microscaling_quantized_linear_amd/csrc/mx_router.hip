@@ -27,14 +27,17 @@
 // error bound, every score of the wavefront's tokens is formed in 64 bits first.  The
 // result is the exact choice either way.  A list that overflows (many equal numbers)
 // gives way to rounds of one expert each.
-// E 256, T 16384, top 8 of 4 of 8 groups: 15.0 us, with 64-bit scores for all and a
-// maximum a round 22.3.
+// Bound: the wavefronts' chains of dependent steps, all tokens in one round of the
+// chip's wavefronts.  E 256, T 16384, top 8 of 4 of 8 groups: 14.0-15.0 us by box (18 MB,
+// 3.8 us of a copy's time); with 64-bit scores for all and a maximum a round 22.3.  A
+// decode step's 16 tokens: 4.0 us, launch and two trips to memory.
 // Groups are scored from LDS, a lane a group, starting at its own place in the group so
 // that the lanes meet different banks.  Wavefronts are independent; LDS serves one
 // wavefront's exchange (operations of a wavefront complete in order).
 //
-// Sums of exponentials are added as chunks of four experts, then over the chunk number's bits in an order that is the same
-// in every form: a token's results do not depend on the other tokens or their number.
+// Sums of exponentials are added as chunks of four experts, then over the chunk
+// number's bits in an order that is the same in every form: a token's results do not
+// depend on the other tokens or their number.
 #include "mx_device.h"
 #include "mx_kernels.h"
 #include "mx_lanes.h"
