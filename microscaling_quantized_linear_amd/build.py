@@ -3,7 +3,8 @@
     python -m microscaling_quantized_linear_amd.build
 
 Objects go to ``_build/`` next to this file; the library is written in-tree as
-``microscaling_quantized_linear_amd/libmx.so``.
+``microscaling_quantized_linear_amd/libmx.so``, the binding's compiled call path
+as ``_mxcall.so`` next to it.
 """
 from __future__ import annotations
 
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmx.so")
+CALL = os.path.join(HERE, "_mxcall.so")
 SOURCES = ["mx_pack.hip", "mx_ingest.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemv_w8.hip",
            "mx_gemm.hip", "mx_static.hip", "mx_norm.hip", "mx_route.hip", "mx_grouped.hip",
            "mx_grouped_gemm.hip", "mx_lora.hip", "mx_gemv_epi.hip", "mx_gemv_w8_epi.hip",
@@ -43,10 +46,26 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_call() -> str:
+    """The binding's call path (csrc/mx_python.cpp): host code against Python's headers.
+    It is imported ahead of torch, so it must not bring in the HIP runtime (hipcc links
+    it): torch loads its own, and two of them in a process do not share a device."""
+    tmp = CALL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "mx_python.cpp"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"build of mx_python.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        call = ex.submit(build_call)
         objs = list(ex.map(_compile, SOURCES))
+        call.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

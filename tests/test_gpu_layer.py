@@ -709,6 +709,45 @@ def test_layer_on_another_stream(g, mx):
             assert torch.equal(x, y)
 
 
+def test_layer_by_either_call_path(g, mx, monkeypatch):
+    """The compiled call path and ctypes: the same launches, so the same bits; a
+    stream as None, an object or a handle; a tensor of another device is refused."""
+    import torch
+    assert mx._mxcall is not None, "_mxcall.so is not built"
+    a, b = Layer(g, mx, 40, key=1), Layer(g, mx, 40, key=1)
+    a.run()
+    side = torch.cuda.Stream()
+    class Elsewhere:                                                            # noqa: E306
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+
+        def data_ptr(self):
+            return 256
+    for compiled in (True, False):
+        if not compiled:
+            monkeypatch.setattr(mx, "_mxcall", None)
+        monkeypatch.setattr(mx.lib(), "direct", {})
+        b.run()
+        torch.cuda.synchronize()
+        for u, v in zip(a.outputs(), b.outputs()):
+            assert torch.equal(u, v)
+        for stream in (side, side.cuda_stream, 0, None):
+            b.ids.zero_()
+            b.wts.zero_()
+            torch.cuda.synchronize()
+            mx.mx_moe_route(12, 40, 3, 1, b.d["logits"], 12, 1, b.d["bias"], 4, 2, 2, True, 1.5, b.ids,
+                            b.wts, stream)
+            torch.cuda.synchronize()
+            assert torch.equal(a.ids, b.ids) and torch.equal(a.wts, b.wts)
+        for at in (4, 7, 14):                          # as the first, a later and the last tensor
+            args = [8, 1, 2, 1, a.d["logits"], 8, 0, None, 1, 1, 1, 1, 1.0, a.ids, a.wts]
+            args[at] = Elsewhere()
+            with pytest.raises(ValueError, match="on cuda:1, not on the current GPU"):
+                mx.mx_moe_route(*args)
+
+
 def test_layer_captured(g, mx):
     """Captured and replayed, with eager work (another layer on the same workspace
     among it) and synchronizations between the replays; two graphs that share a

@@ -193,6 +193,49 @@ def test_binding_refuses_host_tensors():
         mx.mx_moe_route(0, 1, 2, 1, A(0), 8, 0, None, 1, 1, 1, True, 1.0, A(1), A(2), stream=0)
 
 
+@pytest.fixture(params=["compiled", "ctypes"])
+def path(request, monkeypatch):
+    """Either way from Python to the entry points."""
+    if request.param == "compiled":
+        assert mx._mxcall is not None, "_mxcall.so is not built"
+    else:
+        monkeypatch.setattr(mx, "_mxcall", None)
+    monkeypatch.setattr(mx.lib(), "direct", {})
+    return request.param
+
+
+def test_either_call_path_refuses_the_same(path):
+    for call, status, cases in REFUSED:
+        for kw in cases:
+            assert call(**kw) == status, (path, call.__name__, kw)
+
+
+def test_either_call_path_takes_the_same_arguments(path):
+    import torch
+    t = torch.zeros(4096, dtype=torch.int16)
+    args = dict(E=8, T=1, topk=9, type=1, logits=A(0), ldl=8, score=0, bias=None, groups=1, topk_groups=1,
+                group_best=1, renorm=True, scale=1, topk_ids=A(1), topk_weights=A(2), stream=0)
+
+    def run(**kw):
+        return mx.mx_moe_route(**dict(args, **kw))
+
+    class Stream:
+        cuda_stream = 1 << 40
+    for kw in (dict(), dict(renorm=np.bool_(True)), dict(scale=np.float64(2.0)), dict(stream=Stream()),
+               dict(topk=True, E=0), dict(logits=2 ** 64 - 256)):
+        with pytest.raises(mx.MXError):               # topk or E: refused behind the marshalling
+            run(**kw)
+    with pytest.raises(ValueError, match="on cpu, not on the current GPU"):
+        run(topk_weights=t)
+    # what is no number, address, tensor or stream
+    for kw in (dict(E="8"), dict(topk=2.5), dict(scale="1"), dict(scale=None), dict(ldl=None)):
+        with pytest.raises((TypeError, C.ArgumentError)):
+            run(**kw)
+    for kw in (dict(bias="x"), dict(stream="x")):
+        with pytest.raises(AttributeError):
+            run(**kw)
+
+
 # ---- the definitions ---------------------------------------------------------------------
 
 
