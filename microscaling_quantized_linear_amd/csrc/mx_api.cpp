@@ -462,11 +462,15 @@ static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const vo
             if (mx::overlap(sy, in) || mx::overlap(sw, in)) return MX_ERR_UNSUPPORTED;
         if (!mx::apart_or_same(sy, sr) || mx::overlap(sw, sr) || mx::overlap(sw, sy))
             return MX_ERR_UNSUPPORTED;
-        // Without any of it the kernels of mx_linear run, but where the prefill's kernel
-        // with an epilogue has smaller tiles that leave no compute unit without one (M
-        // 1001, N 4096, K 1568: 11.3 against 23.4 us).
+        // Without any of it the kernels of mx_linear run, but where those with an
+        // epilogue have another tile: smaller ones at prefill that leave no compute unit
+        // without one (M 1001, N 4096, K 1568: 11.3 against 23.4 us), four a workgroup
+        // in the GEMV that quantizes inside.
+        const mx::GemvW8Plan w8 = gemv_w8_plan(N, K, M);
         fin.on = end->fn != mx::FN_NONE || end->gated || res ||
-                 (gemm && mx::gemm_epi_tile_n(M, N) < mx::gemm_tile_n(N));
+                 (gemm ? mx::gemm_epi_tile_n(M, N) < mx::gemm_tile_n(N)
+                       : incall && fused_quant_ok(elem, N, K, M) &&
+                             mx::gemv_w8_fused_epi_plan(N, M, w8).g != w8.g);
         fin.fn = end->fn;
         fin.gated = end->gated;
         fin.res = static_cast<const uint16_t *>(res);
@@ -498,8 +502,9 @@ static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const vo
         g.fin = fin;
         log_dispatch("linear: gemv_w8_fused_kernel %s%s, quantization inside (rule %d), "
                      "%d waves x %d steps x %d tiles; M=%lld N=%lld K=%lld",
-                     layout_name(layout), with, rule, w8.nw, w8.spw, w8.g, (long long)M, (long long)N,
-                     (long long)K);
+                     layout_name(layout), with, rule, w8.nw, w8.spw,
+                     fin.on ? mx::gemv_w8_fused_epi_plan(N, M, w8).g : w8.g, (long long)M,
+                     (long long)N, (long long)K);
         return launched(mx::launch_gemv_w8_fused(layout, rule, g, w8, s));
     }
     if (incall && !gemm && !w8.ok) {

@@ -440,14 +440,27 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
 // slower.  Results are
 // identical to mx_quant_act_t16 followed by the even-shape kernel: the same
 // bytes, codes and MFMA order.
+//
+// With an epilogue the launch is often more than a workgroup for each compute unit (a
+// gate and up product's rows), and then it is the activations that cost: every
+// workgroup reads and quantizes all of them, as many bytes as its two tiles of weights.
+// Four tiles a workgroup halve that (gemv_w8_fused_epi_plan; two steps of weights in
+// flight then: 18.5 against 18.8 us at M 16, N 14336, K 7168).  Whole tiles go through
+// registers there too, which leaves room for two workgroups of two tiles a compute unit
+// (M 16, N 28672, K 4096: 24.5 against 26.0 us; with one workgroup each, N 7168, 11.4
+// against 11.5).
+constexpr int fused_waves(bool epi, bool full, int tiles, int steps) {
+    return !epi || !full ? 1 : tiles == 4 && steps > 4 ? 2 : 4;
+}
 template <int LAYOUT, int RULE, int G, int SPW, int NW, bool FULL, bool EPI>
-__global__ void __launch_bounds__(NW * 64) gemv_w8_fused_kernel(GemvW8Args p) {
+__global__ void __launch_bounds__(NW * 64, fused_waves(EPI, FULL, G, SPW))
+gemv_w8_fused_kernel(GemvW8Args p) {
     constexpr int XA = SPW > 4 ? 4 : SPW;              // steps of activations requested first
-    constexpr int WIN = 1;                             // steps of weight chunks in flight
+    constexpr int WIN = EPI && G == 4 && SPW > 4 ? 2 : 1;   // steps of weight chunks in flight
     constexpr int XROW = 272;                          // padded LDS row of one token
     __shared__ v4f red[NW][G][64];
     // whole tiles: activations straight into a ring of four 4 KB LDS slots
-    constexpr bool kXD = FULL && XA == 4;
+    constexpr bool kXD = FULL && XA == 4 && !EPI;
     __shared__ __attribute__((aligned(16))) uint8_t xt[kXD ? 1 : NW][16 * XROW];
     __shared__ __attribute__((aligned(1024))) uint8_t xd[kXD ? NW : 1][kXD ? 4 * 4096 : 16];
 
@@ -927,7 +940,7 @@ template <bool FULL>
 static hipError_t launch_fused(int layout, int rule, const GemvW8Args &a, const GemvW8Plan &pl,
                                hipStream_t st) {
     const dim3 grid((unsigned)(a.N / 16 / pl.g), (unsigned)((a.M + 15) / 16)), block(512);
-    return even_dispatch(pl, [&](auto gc, auto sc) -> hipError_t {
+    auto go = [&](auto gc, auto sc) -> hipError_t {
         constexpr int G = decltype(gc)::value, SPW = decltype(sc)::value;
         if (layout == ROW32) {
             if (rule == RULE_OCP)
@@ -941,13 +954,18 @@ static hipError_t launch_fused(int layout, int rule, const GemvW8Args &a, const 
                 hipLaunchKernelGGL((gemv_w8_fused_kernel<BLK32, RULE_CEIL448, G, SPW, 8, FULL, kEpi>), grid, block, 0, st, a);
         }
         return hipSuccess;
-    });
+    };
+    if constexpr (kEpi)
+        if (pl.g == 4 && pl.spw == 7)
+            return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 7>{});
+    return even_dispatch(pl, go);
 }
 
 hipError_t MX_LAUNCH(launch_gemv_w8_fused)(int layout, int rule, const GemvW8Args &a,
-                                           const GemvW8Plan &pl, hipStream_t st) {
-    if (!kEpi && a.fin.on) return launch_gemv_w8_fused_epi(layout, rule, a, pl, st);
-    if (!gemv_w8_even(a.N, a.K, pl) || a.K % 128 != 0) return hipErrorInvalidValue;
+                                           const GemvW8Plan &given, hipStream_t st) {
+    if (!kEpi && a.fin.on) return launch_gemv_w8_fused_epi(layout, rule, a, given, st);
+    if (!gemv_w8_even(a.N, a.K, given) || a.K % 128 != 0) return hipErrorInvalidValue;
+    const GemvW8Plan pl = kEpi ? gemv_w8_fused_epi_plan(a.N, a.M, given) : given;
     const hipError_t e = a.M % 16 == 0 ? launch_fused<true>(layout, rule, a, pl, st)
                                        : launch_fused<false>(layout, rule, a, pl, st);
     if (e != hipSuccess) return e;

@@ -151,6 +151,7 @@ struct GemvW8Plan {
     bool ok;
 };
 GemvW8Plan plan_gemv_w8(int64_t T, int64_t S, int64_t MB, int nw_force, int g_force);
+GemvW8Plan gemv_w8_fused_epi_plan(int64_t N, int64_t M, const GemvW8Plan &given);
 hipError_t launch_gemv_w8(int layout, bool xt16, const GemvW8Args &a, const GemvW8Plan &plan,
                           hipStream_t stream);
 hipError_t launch_gemv_w8_epi(int layout, bool xt16, const GemvW8Args &a, const GemvW8Plan &plan,

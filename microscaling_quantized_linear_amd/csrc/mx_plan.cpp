@@ -26,6 +26,22 @@ int gemm_epi_tile_n(int64_t M, int64_t N) {
     return gemm_tile_n(N);
 }
 
+// The plan of the GEMV that quantizes inside, with an epilogue: four tiles a workgroup
+// instead of two, for seven steps a wavefront, where that takes fewer rounds of 256
+// workgroups by more than a third, a round of four tiles being about half as long again.
+// Measured, us at four / two (K 7168): one round against two, M 16, N 9216 15.2 / 19.2,
+// N 14336 18.5 / 20.8, N 16384 20.4 / 21.6, M 32, N 7168 14.6 / 19.9; two against four,
+// M 64, N 7168 27.8 / 37.5; three against five, M 40, N 12288 42.5 / 48.4.  Not where it
+// is one against one, N 8192 14.8 / 12.0, or two against three, N 20480 31.6 / 29.1 (M
+// 48, N 7168: 26.4 / 28.4).  Eight steps a wavefront lose (N 16384, K 8192: 29.6 / 27.6).
+GemvW8Plan gemv_w8_fused_epi_plan(int64_t N, int64_t M, const GemvW8Plan &given) {
+    GemvW8Plan pl = given;
+    const int64_t T = N / 16, MB = (M + 15) / 16;
+    auto rounds = [&](int64_t g) { return (T / g * MB + 255) / 256; };
+    if (pl.spw == 7 && pl.g == 2 && T % 4 == 0 && 3 * rounds(4) < 2 * rounds(2)) pl.g = 4;
+    return pl;
+}
+
 // Launch plan for T tiles, S steps and MB 16-token grid rows: tiles per
 // workgroup G in {4, 2, 1} (the largest that still gives about one
 // workgroup per compute unit, measured best on MI355X), up to eight

@@ -513,6 +513,28 @@ def test_linear_without_epilogue_is_mx_linear(g, mx):
             assert np.array_equal(y[0], y[1]) and np.array_equal(y[0], y[2])
 
 
+@pytest.mark.parametrize("layout,M,N", [(0, 64, 2112), (1, 50, 2112), (0, 61, 2080), (1, 49, 2176)])
+def test_linear_epilogue_more_than_one_round(g, mx, layout, M, N):
+    """The GEMV that quantizes inside at more workgroups than compute units: four tiles
+    a workgroup (two where the tiles do not divide), whole and partial token tiles.
+    Without an epilogue the bits are mx_linear's."""
+    K = 7168
+    r = rng(43, layout, M, N)
+    lin = Lin(g, r, 0, layout, M, N, K, MXFP8, rule=M % 2)
+    for n, (kind, gated) in enumerate(((ref.SILU, True), (ref.GELU, False), (ref.NONE, False),
+                                       (ref.RELU2, True))):
+        bias = bf16(r, N) if n % 2 else None
+        res = bf16(r, M, N // 2 if gated else N, scale=2) if n else None
+        y = lin.run(mx, "x", bias, kind, gated, res, pad=8 * n)
+        out, tol = ref.epilogue(lin.z, lin.dz, bias, kind, gated, res)
+        ops_ref.assert_within(y, out, tol, f"fn {kind} gated {gated}")
+        if res is not None:
+            assert np.array_equal(lin.run(mx, "x", bias, kind, gated, res, pad=8 * n, inplace=True), y)
+    bias = bf16(r, N)
+    want = g.linear(0, layout, N, K, *lin.packed, MXFP8, x=lin.x, bias=bias, rule=M % 2)
+    assert np.array_equal(lin.run(mx, "x", bias, 0, False, None), want)
+
+
 def test_linear_epilogue_values(g, mx):
     """Sums over the whole range of the activations, far tails and beyond bf16 among
     them: a one-hot x hands z to each function exactly."""
