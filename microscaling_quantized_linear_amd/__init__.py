@@ -5,7 +5,7 @@ in-tree by :mod:`microscaling_quantized_linear_amd.build`).  The functions
 here only marshal arguments: tensors are passed as device pointers, streams
 as HIP stream handles, and every step of the computation runs in the HIP
 kernels.  The calls of :func:`_direct` are marshalled by a compiled module
-(``_mxcall.so``, built with the library) or, without it, by ctypes as the
+(``_mxcall``, built with the library) or, without it, by ctypes as the
 others; the entry points are the same.  There is no fallback: if ``libmx.so`` is missing or a call fails,
 an exception is raised.
 

@@ -4,7 +4,7 @@
 
 Objects go to ``_build/`` next to this file; the library is written in-tree as
 ``microscaling_quantized_linear_amd/libmx.so``, the binding's compiled call path
-as ``_mxcall.so`` next to it.
+as ``_mxcall`` (with this Python's extension suffix) next to it.
 """
 from __future__ import annotations
 
@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmx.so")
-CALL = os.path.join(HERE, "_mxcall.so")
+CALL = os.path.join(HERE, "_mxcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["mx_pack.hip", "mx_ingest.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemv_w8.hip",
            "mx_gemm.hip", "mx_static.hip", "mx_norm.hip", "mx_route.hip", "mx_grouped.hip",
            "mx_grouped_gemm.hip", "mx_lora.hip", "mx_gemv_epi.hip", "mx_gemv_w8_epi.hip",

@@ -197,7 +197,7 @@ def test_binding_refuses_host_tensors():
 def path(request, monkeypatch):
     """Either way from Python to the entry points."""
     if request.param == "compiled":
-        assert mx._mxcall is not None, "_mxcall.so is not built"
+        assert mx._mxcall is not None, "_mxcall is not built"
     else:
         monkeypatch.setattr(mx, "_mxcall", None)
     monkeypatch.setattr(mx.lib(), "direct", {})
