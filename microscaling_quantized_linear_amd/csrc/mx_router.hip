@@ -23,16 +23,19 @@
 //     lower expert.
 // With a bias c comes from fast fp32 scores first: groups and the list go by them, the
 // list with the fast scores' error bound added to it, and the list's entries are then
-// formed in 64 bits.  Where the last kept and the first dropped group are nearer than the
-// error bound, every score of the wavefront's tokens is formed in 64 bits first.  The
-// result is the exact choice either way.  A list that overflows (many equal numbers)
+// formed in 64 bits.  Where a token's last kept and first dropped group are nearer than
+// the error bound, the scores that may be among their groups' best are formed in 64 bits
+// first (every score of the wavefront's tokens: 15.0 us instead of 14.0 for the call
+// below, whose end waits for the few wavefronts that this happens to).  The result is
+// the exact choice either way.  A list that overflows (many equal numbers)
 // gives way to rounds of one expert each.
 // Bound: the wavefronts' chains of dependent steps, all tokens in one round of the
-// chip's wavefronts.  E 256, T 16384, top 8 of 4 of 8 groups: 14.0-15.0 us by box (18 MB,
+// chip's wavefronts.  E 256, T 16384, top 8 of 4 of 8 groups: 13.2-14.0 us by box (18 MB,
 // 3.8 us of a copy's time); with 64-bit scores for all and a maximum a round 22.3.  A
 // decode step's 16 tokens: 4.0 us, launch and two trips to memory.
-// Groups are scored from LDS, a lane a group, starting at its own place in the group so
-// that the lanes meet different banks.  Wavefronts are independent; LDS serves one
+// Groups of 4, 8, .. 64 experts are scored in registers, over the lanes that hold them
+// (E 64, T 16384, 8 groups: 8.0 us, the other form 8.4), others from LDS, a lane a group, starting at its own place
+// in the group so that the lanes meet different banks.  Wavefronts are independent; LDS serves one
 // wavefront's exchange (operations of a wavefront complete in order).
 //
 // Sums of exponentials are added as chunks of four experts, then over the chunk
@@ -239,9 +242,56 @@ __global__ void __launch_bounds__(64 * kRouteWaves, 4) route_kernel(RouteArgs p)
         return __uint_as_float(s & 0x80000000u ? s ^ 0x80000000u : ~s);
     };
 
+    // this lane's experts (bit 4 c + d) that may be among their groups' best
+    uint32_t near = ~0u;
     // the groups that are kept, as bits of g; `doubt` where the fast scores do not tell
     auto keep_groups = [&](bool &doubt) -> uint64_t {
-        const int G = p.groups, n = p.per_group;
+        const int G = p.groups, n = p.per_group, span = n / 4;
+        if (n % 4 == 0 && (span & (span - 1)) == 0 && span <= (LPT < 16 ? LPT : 16)) {
+            // the group's chunks lie in `span` neighbouring lanes (uniform)
+            float m1[C], m2[C];                           // the two largest
+            auto join = [&](int c, float u1, float u2) {
+                m2[c] = __builtin_fmaxf(__builtin_fminf(m1[c], u1), __builtin_fmaxf(m2[c], u2));
+                m1[c] = __builtin_fmaxf(m1[c], u1);
+            };
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                m1[c] = __builtin_fmaxf(f[c][0], f[c][1]);
+                m2[c] = __builtin_fminf(f[c][0], f[c][1]);
+                join(c, __builtin_fmaxf(f[c][2], f[c][3]), __builtin_fminf(f[c][2], f[c][3]));
+            }
+            auto meet = [&](auto ctrl) {
+                constexpr int CTRL = decltype(ctrl)::value;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    join(c, __uint_as_float(dpp<CTRL>(__float_as_uint(m1[c]))),
+                         __uint_as_float(dpp<CTRL>(__float_as_uint(m2[c]))));
+            };
+            if (span > 1) meet(std::integral_constant<int, kSwap1>{});
+            if (span > 2) meet(std::integral_constant<int, kSwap2>{});
+            if (span > 4) meet(std::integral_constant<int, kHalfMirror>{});
+            if (span > 8) meet(std::integral_constant<int, kRotate8>{});
+            if constexpr (BIAS) {
+                // the last of a group's best is at least its fast score less the error,
+                // and an expert's fast score at least its own less as much
+                near = 0;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float last = p.group_best == 2 ? m2[c] : m1[c];
+                    const float least = last - 3.0f * error(last);
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        near |= f[c][d] > -INFINITY && f[c][d] >= least ? 1u << (4 * c + d) : 0u;
+                }
+            }
+            const int shift = __ffs(span) - 1;
+            if ((i & (span - 1)) == 0)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int g = (i + LPT * c) >> shift;
+                    if (g < G) gs[g] = p.group_best == 2 ? m1[c] + m2[c] : m1[c];
+                }
+        } else
         for (int g = i; g < G; g += LPT) {
             float m1 = -INFINITY, m2 = -INFINITY;         // the two largest so far
             auto take = [&](float v) {
@@ -334,27 +384,31 @@ __global__ void __launch_bounds__(64 * kRouteWaves, 4) route_kernel(RouteArgs p)
             *reinterpret_cast<v4f *>(cs + 4 * (i + LPT * c)) = v4f{x[c][0], x[c][1], x[c][2], x[c][3]};
         wave_order();
     };
-    // every c with its score from 64 bits (in a loop: the code is seldom run)
-    auto exact = [&]() {
+    // c with its score from 64 bits, for the experts `which` of this lane
+    auto exact = [&](const uint32_t which) {
         keep_logits();
-#pragma unroll 2
-        for (int k = 0; k < 4 * C; ++k) {
-            const int e = 4 * (i + LPT * (k / 4)) + k % 4;
-            const float v = cs[e], b = e < E ? p.bias[e] : 0.0f;
-            cs[e] = v > -INFINITY ? clean(score(v) + b) : -INFINITY;
+        uint32_t left = which;
+        while (__ballot(left != 0u)) {
+            if (left) {
+                const int k = __ffs((int)left) - 1, e = 4 * (i + LPT * (k / 4)) + k % 4;
+                left &= left - 1u;
+                const float v = cs[e], b = e < E ? p.bias[e] : 0.0f;
+                cs[e] = v > -INFINITY ? clean(score(v) + b) : -INFINITY;
+            }
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const v4f v = *reinterpret_cast<const v4f *>(cs + 4 * (i + LPT * c));
 #pragma unroll
-            for (int d = 0; d < 4; ++d) f[c][d] = v[d];
+            for (int d = 0; d < 4; ++d) f[c][d] = which >> (4 * c + d) & 1u ? v[d] : f[c][d];
         }
     };
+    constexpr uint32_t kEvery = C == 8 ? ~0u : (1u << (4 * C % 32)) - 1u;
     bool doubt = false;
     keys(doubt);
     if constexpr (BIAS)
         if (__ballot(doubt && live)) {
-            exact();
+            exact(doubt ? near & kEvery : 0u);
             keys(doubt);
         }
     if constexpr (BIAS) keep_logits();                    // without a bias they stand there
@@ -449,7 +503,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves, 4) route_kernel(RouteArgs p)
         }
     } else {
         // ---- by (number, lower expert first), one a round ----
-        if constexpr (BIAS) exact();
+        if constexpr (BIAS) exact(kEvery);
         keys(doubt);
         for (int r = 0; r < p.topk; ++r) {
             uint32_t m = 0;

@@ -168,6 +168,26 @@ def test_route_near_ties(g, mx):
         check_route(run_route(g, mx, x, 1, bias, topk=8), x, 1, bias, topk=8)
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (96, 8), (256, 8), (256, 4), (128, 32)])
+def test_route_near_tied_groups(g, mx, E, groups):
+    """Groups whose scores are a last place apart, in every token or in a few of them:
+    those of the correctly rounded scores are kept."""
+    r = rng(5, E, groups)
+    T = 1500
+    s = 0.5 + np.float64(2.0) ** -24 * r.integers(0, 6, (T, E))
+    x = np.log(s / (1 - s)).astype(np.float32)
+    few = (1.5 * r.standard_normal((T, E))).astype(np.float32)
+    few[::97] = x[::97]
+    few[5::97, E // groups:] = -INF
+    half = np.full(E, 0.25, np.float32)
+    for v in (x, few):
+        for score in (0, 1):
+            for bias in (half, (0.1 * r.standard_normal(E)).astype(np.float32)):
+                for best in (1, 2):
+                    kw = dict(groups=groups, keep=groups // 2, best=best, topk=6)
+                    check_route(run_route(g, mx, v, score, bias, **kw), v, score, bias, **kw)
+
+
 def test_route_tokens_do_not_depend_on_the_call(g, mx):
     """A token alone, in a small call and in a large one (another form): the same bits."""
     for E in (24, 64, 100, 256, 512):
