@@ -648,7 +648,7 @@ mx_status mx_moe_route(int64_t E, int64_t T, int64_t topk, int type, const void 
  *   post_weight (device, nullable) bf16 [K], 16-byte aligned
  *   gate     (device, nullable) bf16 [gates, ldg], the rules of x; g = gate_ids[m], or
  *            0 without gate_ids; where g is outside [0, gates) the block adds nothing:
- *            s = T(alpha * residual)
+ *            s = T(alpha * residual), whatever x, post_weight and the gates hold
  *   gate_ids (device, nullable; unused without a gate) int32 [M]
  *   stream_type  of residual and sum (mx_float)
  *   residual (device, nullable) [M, ldr], 16-byte aligned, rows a multiple of 16 bytes

@@ -84,11 +84,7 @@ __global__ void __launch_bounds__(64 * kBlockWaves) block_norm_kernel(BlockNormA
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int w = wave % WPR;
     const int K = (int)p.K, S = (K + 127) / 128, Q = (S + 3) / 4;
-    const __amdgpu_buffer_rsrc_t pr = make_rsrc(p.post, p.post ? (uint32_t)K * 2u : 0u);
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.weight, p.weight ? (uint32_t)K * 2u : 0u);
-    // What is not there costs no branch: an empty resource reads zeros, the vectors'
-    // offset is then 1.
-    const float poff = p.post ? p.offset : 1.0f, goff = p.gate ? 0.0f : 1.0f;
     auto seg = [&](int i) -> uint32_t { return (uint32_t)(1024 * (w + WPR * i) + 16 * lane); };
 
     int64_t m = (int64_t)blockIdx.x * ROWS + wave / WPR;
@@ -101,16 +97,22 @@ __global__ void __launch_bounds__(64 * kBlockWaves) block_norm_kernel(BlockNormA
     const bool live = m < p.M;                            // T16: rows past M pad the last tile
     const uint32_t rowb = live ? (uint32_t)K * 2u : 0u;
     const int64_t mr = live ? m : 0;
-    // a gate's number outside [0, gates): the block adds nothing, x reads as zeros
+    // a gate's number outside [0, gates): the block adds nothing.  x reads as zeros, and
+    // neither a gate nor the post weight is there (their infinities would make NaN of it)
     int64_t gid = 0;
     if (p.gate && p.gate_ids && live) gid = p.gate_ids[m];
     const bool out = p.gate && (gid < 0 || gid >= p.gates);
+    // What is not there costs no branch: an empty resource reads zeros, the vectors'
+    // offset is then 1.
+    const bool post = p.post && !out, gated = p.gate && !out;
+    const float poff = post ? p.offset : 1.0f, goff = gated ? 0.0f : 1.0f;
+    const __amdgpu_buffer_rsrc_t pr = make_rsrc(p.post, post ? (uint32_t)K * 2u : 0u);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + mr * p.ldx, out ? 0u : rowb);
     const __amdgpu_buffer_rsrc_t rr = make_rsrc(
         p.res ? static_cast<const uint8_t *>(p.res) + mr * p.ldr * SIZE : nullptr,
         p.res ? rowb / 2 * SIZE : 0u);
     const __amdgpu_buffer_rsrc_t gr = make_rsrc(
-        p.gate ? p.gate + (out ? 0 : gid) * p.ldg : nullptr, p.gate ? (uint32_t)K * 2u : 0u);
+        p.gate ? p.gate + (out ? 0 : gid) * p.ldg : nullptr, gated ? (uint32_t)K * 2u : 0u);
     v4u x[NS], res[NS][RN], gate[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) x[i] = load16<AUX>(xr, seg(i));
