@@ -278,7 +278,8 @@ mx_status mx_linear(int elem, int layout, int64_t N, int64_t K,
 
 /* Activations of mx_linear_epilogue: z; max(z, 0); max(z, 0)^2; z / (1 + e^-z);
  * z Phi(z), Phi the normal distribution; z / 2 (1 + tanh(sqrt(2 / pi)
- * (z + 0.044715 z^3))). */
+ * (z + 0.044715 z^3))).  At an infinite z they take their limits: +inf, and 0 on the
+ * left of all but the first; NaN stays NaN. */
 typedef enum {
     MX_FN_NONE = 0,
     MX_FN_RELU = 1,

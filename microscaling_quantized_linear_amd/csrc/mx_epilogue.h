@@ -7,45 +7,54 @@
 // without one stay as they are.
 #pragma once
 
+#include <cfloat>
+
 #include "mx_device.h"
 #include "mx_kernels.h"
 
 namespace mx {
 
 // The activations by what they cost: none, relu and relu2 are comparisons and a
-// product; silu and tanh-gelu are z times a logistic function of an odd cubic
-// (0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))), so one form with two coefficients
-// serves both; erf-gelu has its own.  (KIND_NONE: the prefill kernel's form for none.)
-enum { KIND_SIMPLE = 0, KIND_LOGISTIC = 1, KIND_ERF = 2, KIND_NONE = 3 };
+// product; silu and tanh-gelu are z times a logistic function, of z and of an odd
+// cubic (0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))), each in a form of its own: a cubic
+// with a zero coefficient is NaN where z is infinite; erf-gelu has its own.
+// (KIND_NONE: the prefill kernel's form for none.)
+enum { KIND_SIMPLE = 0, KIND_SILU = 1, KIND_TANH = 2, KIND_ERF = 3, KIND_NONE = 4 };
 __host__ __device__ inline int fn_kind(int fn) {
-    return fn == FN_GELU ? KIND_ERF : fn >= FN_SILU ? KIND_LOGISTIC : KIND_SIMPLE;
+    return fn == FN_GELU        ? KIND_ERF
+           : fn == FN_GELU_TANH ? KIND_TANH
+           : fn == FN_SILU      ? KIND_SILU
+                                : KIND_SIMPLE;
 }
 
 struct FnCoef {
-    float a, b;       // KIND_LOGISTIC: z / (1 + 2^(z (a + b z^2)))
     bool relu, square;
 };
 __device__ inline FnCoef fn_coef(int fn) {
-    constexpr float kLog2e = 1.4426950408889634f;
     FnCoef c;
-    // silu: a = -log2 e; tanh-gelu: -2 sqrt(2 / pi) (z + 0.044715 z^3) log2 e
-    c.a = fn == FN_GELU_TANH ? -1.5957691216057308f * kLog2e : -kLog2e;
-    c.b = fn == FN_GELU_TANH ? -1.5957691216057308f * 0.044715f * kLog2e : 0.0f;
     c.relu = fn == FN_RELU || fn == FN_RELU2;
     c.square = fn == FN_RELU2;
     return c;
 }
 
-// f(z).  KIND_LOGISTIC: v_exp_f32 and v_rcp_f32 are within a last place, the
-// exponent's rounding adds |z| 2^-23: far below the bf16 rounding that follows.
+// f(z).  KIND_SILU, KIND_TANH: z / (1 + 2^t), t of the other sign than z; v_exp_f32 and
+// v_rcp_f32 are within a last place, the exponent's rounding adds |t| 2^-23: far below
+// the bf16 rounding that follows.  Infinite z give the limits: 2^-inf is 0 and z itself
+// remains, and on the left the largest number stands for z, whose quotient is 0 (NaN
+// stays in t).
 // KIND_ERF: z Phi(z) with Phi(-t) = exp(-t^2 / 2) p(1 / (1 + 0.42 t / sqrt 2)), p of
 // degree 6 fitted to 0.5 erfcx in relative error (2.1e-6 in fp32 for t <= 14, where
 // bf16 ends), so the negative tail keeps its relative precision too.
 template <int KIND>
 __device__ inline float fn_value(float z, const FnCoef &c) {
-    if constexpr (KIND == KIND_LOGISTIC) {
-        const float e = __builtin_amdgcn_exp2f(z * __builtin_fmaf(c.b * z, z, c.a));
-        return z * __builtin_amdgcn_rcpf(1.0f + e);
+    if constexpr (KIND == KIND_SILU || KIND == KIND_TANH) {
+        constexpr double kLog2e = 1.4426950408889634, kTanh = -1.5957691216057308 * kLog2e;
+        // tanh-gelu: -2 sqrt(2 / pi) (z + 0.044715 z^3) log2 e
+        const float t = KIND == KIND_SILU
+                            ? z * (float)-kLog2e
+                            : z * __builtin_fmaf(z * (float)(0.044715 * kTanh), z, (float)kTanh);
+        const float e = __builtin_amdgcn_exp2f(t);
+        return __builtin_fmaxf(z, -FLT_MAX) * __builtin_amdgcn_rcpf(1.0f + e);
     } else if constexpr (KIND == KIND_ERF) {
         const float t = __builtin_fminf(__builtin_fabsf(z), 32.0f);
         const float u = __builtin_amdgcn_rcpf(__builtin_fmaf(t, 0.42f * 0.70710678f, 1.0f));
@@ -70,7 +79,8 @@ __device__ inline float fn_value(float z, const FnCoef &c) {
 __device__ inline float fn_any(int fn, float z, const FnCoef &c) {
     const int kind = fn_kind(fn);
     if (kind == KIND_SIMPLE) return fn_value<KIND_SIMPLE>(z, c);
-    if (kind == KIND_LOGISTIC) return fn_value<KIND_LOGISTIC>(z, c);
+    if (kind == KIND_SILU) return fn_value<KIND_SILU>(z, c);
+    if (kind == KIND_TANH) return fn_value<KIND_TANH>(z, c);
     return fn_value<KIND_ERF>(z, c);
 }
 

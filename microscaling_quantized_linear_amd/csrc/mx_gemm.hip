@@ -505,18 +505,21 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
         };
         using KN = std::integral_constant<int, KIND_NONE>;
         using K0 = std::integral_constant<int, KIND_SIMPLE>;
-        using K1 = std::integral_constant<int, KIND_LOGISTIC>;
-        using K2 = std::integral_constant<int, KIND_ERF>;
+        using K1 = std::integral_constant<int, KIND_SILU>;
+        using K2 = std::integral_constant<int, KIND_TANH>;
+        using K3 = std::integral_constant<int, KIND_ERF>;
         const int kind = fn_kind(p.fin.fn);
         if (p.fin.gated) {
             if (kind == KIND_SIMPLE) finish(K0{}, std::true_type{});
-            else if (kind == KIND_LOGISTIC) finish(K1{}, std::true_type{});
-            else finish(K2{}, std::true_type{});
+            else if (kind == KIND_SILU) finish(K1{}, std::true_type{});
+            else if (kind == KIND_TANH) finish(K2{}, std::true_type{});
+            else finish(K3{}, std::true_type{});
         } else {
             if (p.fin.fn == FN_NONE) finish(KN{}, std::false_type{});
             else if (kind == KIND_SIMPLE) finish(K0{}, std::false_type{});
-            else if (kind == KIND_LOGISTIC) finish(K1{}, std::false_type{});
-            else finish(K2{}, std::false_type{});
+            else if (kind == KIND_SILU) finish(K1{}, std::false_type{});
+            else if (kind == KIND_TANH) finish(K2{}, std::false_type{});
+            else finish(K3{}, std::false_type{});
         }
         return;
     }

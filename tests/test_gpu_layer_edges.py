@@ -1,10 +1,13 @@
 """Edges of the operators between a layer's products that need cases of their own:
-gates and weights that are not finite."""
+gates and weights that are not finite, infinite sums."""
 import numpy as np
 import pytest
 
-from test_gpu_layer import (MXFP8, NAN16, block_inputs, check_block, g, mx, rng,  # noqa: F401
-                            run_block)
+import layer_ref as ref
+import ops_ref
+import oracle
+from test_gpu_layer import (BF16, MXFP8, NAN16, Lin, block_inputs, check_block, g,  # noqa: F401
+                            mx, rng, run_block)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +42,58 @@ def test_block_norm_rows_without_a_gate(g, mx, with_post, fp32):
                 # against a call in which gates, weight and x are ordinary
                 check_block([rows(v) for v in got], np.full_like(i["x"][out], 0x3F80), i["post"],
                             np.full_like(i["gate"], 0x3F80), i["gids"][out], rows(res), *a[5:])
+
+
+# ---- the linear's epilogue -----------------------------------------------------------
+
+
+FORMS = [  # elem, layout, M, N, K, act, form: every kernel with an epilogue
+    (0, 0, 3, 64, 96, BF16, "x"), (1, 0, 4, 64, 4096, BF16, "x"),
+    (0, 1, 16, 64, 1024, MXFP8, "x"), (0, 0, 5, 64, 1024, MXFP8, "x"), (0, 1, 9, 64, 1568, MXFP8, "x"),
+    (0, 0, 9, 64, 1024, MXFP8, "given"), (0, 1, 9, 64, 1024, MXFP8, "t16"),
+    (0, 0, 6, 64, 8224, MXFP8, "x"),
+    (0, 1, 70, 64, 160, MXFP8, "t16"), (0, 0, 1025, 3600, 160, MXFP8, "t16"),
+    (0, 1, 2100, 3616, 160, MXFP8, "t16")]
+
+
+def of_bias(g, elem, layout, M, N, K, act):
+    """A product whose sums are the bias: x is zeros."""
+    lin = Lin(g, rng(81, elem, layout, M, N, K), elem, layout, 1, N, K, act)
+    lin.sizes, lin.x = (M, N, K), np.zeros((M, K), np.uint16)
+    if act != BF16:
+        lin.q, lin.c = oracle.quant_act(lin.x, 0)
+    return lin
+
+
+def values(bits):
+    return ops_ref.f64(np.asarray(bits, np.uint16))
+
+
+@pytest.mark.parametrize("elem,layout,M,N,K,act,form", FORMS)
+def test_linear_epilogue_infinite_sums(g, mx, elem, layout, M, N, K, act, form):
+    """An infinite sum gives the activation's limit (+inf, or 0 on the left), a NaN a
+    NaN, the largest numbers themselves."""
+    lin = of_bias(g, elem, layout, M, N, K, act)
+    z16 = np.resize(np.array([PINF16, NINF16, 0x7FC0, 0x7F7F, 0xFF7F, 0x6000, 0xE000, 0x3F80],
+                             np.uint16), N)
+    z = values(z16)
+    for kind in range(6):
+        with np.errstate(invalid="ignore", over="ignore"):
+            want = ref.fn(kind, np.where(np.isfinite(z), z, 1.0))
+        if kind != ref.NONE:
+            want = np.where(z == -np.inf, 0.0, want)
+        else:
+            want = np.where(z == -np.inf, z, want)
+        want = np.where(z == np.inf, z, np.where(np.isnan(z), z, want))
+        y = values(lin.run(mx, form, z16, kind, False, None))
+        # the gate's partners are 2 and 3 in turn: z stands at the even rows
+        paired = np.stack([z16[:N // 2], np.resize(np.array([0x4000, 0xC040], np.uint16), N // 2)], 1)
+        yg = values(lin.run(mx, form, np.ascontiguousarray(paired).reshape(-1), kind, True, None))
+        for got, exact in ((y, want), (yg, want[:N // 2] * np.resize([2.0, -3.0], N // 2))):
+            exact = np.broadcast_to(exact, got.shape)
+            big = np.isinf(exact) | (np.abs(exact) > 2.0 ** 128 * (1 - 2.0 ** -9))
+            near = np.where(big | np.isnan(exact), 0.0, exact)
+            assert np.array_equal(np.isnan(got), np.isnan(exact)), kind
+            assert np.array_equal(got[big], np.sign(exact[big]) * np.inf), kind
+            err = np.abs(np.where(big | np.isnan(exact), 0.0, got) - near)
+            assert (err <= (2.0 ** -8 + 2.0 ** -13) * np.abs(near) + 2.0 ** -126).all(), kind
