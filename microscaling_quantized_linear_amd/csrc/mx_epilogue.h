@@ -37,24 +37,29 @@ __device__ inline FnCoef fn_coef(int fn) {
     return c;
 }
 
-// f(z).  KIND_SILU, KIND_TANH: z / (1 + 2^t), t of the other sign than z; v_exp_f32 and
-// v_rcp_f32 are within a last place, the exponent's rounding adds |t| 2^-23: far below
-// the bf16 rounding that follows.  Infinite z give the limits: 2^-inf is 0 and z itself
-// remains, and on the left the largest number stands for z, whose quotient is 0 (NaN
-// stays in t).
+// f(z).  KIND_SILU, KIND_TANH: z / (1 + 2^t), t of the other sign than z, both parts
+// times 2^-8.  v_rcp_f32 gives 0 for a divisor above 2^126, which is 2^t alone at z =
+// -87.3 (silu) where z / 2^t is 2^-119 yet; scaled, the divisor gets there at t = 134
+// only, where the quotient is below 2^-126.  v_exp_f32 and v_rcp_f32 are within a last
+// place; with the exponent's roundings the value is within 4e-6 (silu) and 1.1e-5 of
+// itself at the left end, within 3e-7 right of zero (7e-6 where z 2^-8 is below
+// 2^-126): far below the bf16 rounding that follows.  Infinite z give the limits:
+// 2^-inf is 0 and z itself remains, and on the left the largest number stands for z,
+// whose quotient is 0 (NaN stays in t).
 // KIND_ERF: z Phi(z) with Phi(-t) = exp(-t^2 / 2) p(1 / (1 + 0.42 t / sqrt 2)), p of
-// degree 6 fitted to 0.5 erfcx in relative error (2.1e-6 in fp32 for t <= 14, where
-// bf16 ends), so the negative tail keeps its relative precision too.
+// degree 6 fitted to 0.5 erfcx in relative error (1.8e-6; with the roundings, the
+// exponent's two among them, 4e-6 for t <= 8 and 1e-5 at t = 13, where |z Phi(z)| is
+// 2^-126), so the negative tail keeps its relative precision too.
 template <int KIND>
 __device__ inline float fn_value(float z, const FnCoef &c) {
     if constexpr (KIND == KIND_SILU || KIND == KIND_TANH) {
         constexpr double kLog2e = 1.4426950408889634, kTanh = -1.5957691216057308 * kLog2e;
         // tanh-gelu: -2 sqrt(2 / pi) (z + 0.044715 z^3) log2 e
-        const float t = KIND == KIND_SILU
-                            ? z * (float)-kLog2e
-                            : z * __builtin_fmaf(z * (float)(0.044715 * kTanh), z, (float)kTanh);
-        const float e = __builtin_amdgcn_exp2f(t);
-        return __builtin_fmaxf(z, -FLT_MAX) * __builtin_amdgcn_rcpf(1.0f + e);
+        const float a = KIND == KIND_SILU
+                            ? (float)-kLog2e
+                            : __builtin_fmaf(z * (float)(0.044715 * kTanh), z, (float)kTanh);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, a, -8.0f));       // 2^(t - 8)
+        return __builtin_fmaxf(z * 0x1p-8f, -FLT_MAX) * __builtin_amdgcn_rcpf(0x1p-8f + e);
     } else if constexpr (KIND == KIND_ERF) {
         const float t = __builtin_fminf(__builtin_fabsf(z), 32.0f);
         const float u = __builtin_amdgcn_rcpf(__builtin_fmaf(t, 0.42f * 0.70710678f, 1.0f));

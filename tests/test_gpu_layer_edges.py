@@ -1,5 +1,6 @@
 """Edges of the operators between a layer's products that need cases of their own:
-gates and weights that are not finite, infinite sums."""
+gates and weights that are not finite, sums infinite or far out in an activation's
+tails."""
 import numpy as np
 import pytest
 
@@ -97,3 +98,22 @@ def test_linear_epilogue_infinite_sums(g, mx, elem, layout, M, N, K, act, form):
             assert np.array_equal(got[big], np.sign(exact[big]) * np.inf), kind
             err = np.abs(np.where(big | np.isnan(exact), 0.0, got) - near)
             assert (err <= (2.0 ** -8 + 2.0 ** -13) * np.abs(near) + 2.0 ** -126).all(), kind
+
+
+@pytest.mark.parametrize("elem,layout,M,N,K,act,form", [f for f in FORMS if f[2] < 100])
+def test_linear_epilogue_tails(g, mx, elem, layout, M, N, K, act, form):
+    """f within 2^-14 of its value, relative, down to 2^-126, and one bf16 rounding: at
+    every bf16 number from -4 to -128 and at small ones."""
+    small = (0x0080 + 64 * np.arange(96)) | np.array([[0], [0x8000]])           # from 2^-126
+    z16 = np.concatenate([np.arange(0xC080, 0xC300), small.reshape(-1)]).astype(np.uint16)
+    N = (len(z16) + 31) // 32 * 32
+    z16 = np.resize(z16, N)
+    lin = of_bias(g, elem, layout, M, N, K, act)
+    z = values(z16)
+    for kind in (ref.SILU, ref.GELU, ref.GELU_TANH):
+        want = ref.fn(kind, z)
+        y = values(lin.run(mx, form, z16, kind, False, None))
+        of_f = np.where(np.abs(want) >= 2.0 ** -126, 2.0 ** -14 * np.abs(want), 2.0 ** -126)
+        err = np.abs(y - want)
+        bad = err > of_f + 2.0 ** -8 * (np.abs(want) + of_f)
+        assert not bad.any(), (kind, z[bad.any(0)][:8], y[bad][:8])
