@@ -166,7 +166,16 @@ int env_choice(const char *name) {
     return (v == 1 || v == 2 || v == 4 || v == 8) ? v : 0;
 }
 
-// Launch shape of the GEMV (see mx_kernels.h).  MX_GEMV_WAVES, MX_GEMV_CHUNK
+// Launch shape of the dense GEMV (see mx_kernels.h) by its steps of K; gemv_shape has
+// what was measured.
+mx::GemvShape dense_shape(int64_t S) {
+    if (S >= 32) return {8, 4, 2};
+    if (S >= 16) return {4, 4, 1};
+    if (S >= 8) return {2, 8, 1};
+    return {S >= 2 ? 2 : 1, 2, 1};
+}
+
+// Launch shape of the GEMV.  MX_GEMV_WAVES, MX_GEMV_CHUNK
 // and MX_GEMV_TILES override it (tuning sweeps only; read once).
 // Defaults measured on MI355X with graph-replayed launches: long K (S >= 32
 // steps, e.g. 7168) 8 waves x chunks of 4 steps x 2 tiles; 16 <= S < 32 4
@@ -179,20 +188,21 @@ int env_choice(const char *name) {
 mx::GemvShape gemv_shape(int64_t S, bool moe) {
     static const int f_nw = env_choice("MX_GEMV_WAVES"), f_chunk = env_choice("MX_GEMV_CHUNK"),
                      f_tiles = env_choice("MX_GEMV_TILES");
-    mx::GemvShape g;
-    if (moe)
-        g = {S >= 16 ? 4 : S >= 2 ? 2 : 1, 2, 4};
-    else if (S >= 32)
-        g = {8, 4, 2};
-    else if (S >= 16)
-        g = {4, 4, 1};
-    else if (S >= 8)
-        g = {2, 8, 1};
-    else
-        g = {S >= 2 ? 2 : 1, 2, 1};
+    mx::GemvShape g = moe ? mx::GemvShape{S >= 16 ? 4 : S >= 2 ? 2 : 1, 2, 4} : dense_shape(S);
     if (f_nw) g.nw = f_nw;
     if (f_chunk) g.chunk = f_chunk < 2 ? 2 : f_chunk;
     if (f_tiles) g.tiles = f_tiles > 4 ? 4 : f_tiles;
+    return g;
+}
+
+// The same of a call with an epilogue, which has kernels of these shapes alone and does
+// not follow the overrides.  At long K one tile a workgroup while every tile has a
+// compute unit of its own (N 4096, K 7168: e4m3 11.2 -> 8.8 us, e2m1 8.5 -> 7.4); else
+// two, which share the activations (N 7168, K 4096: 8.6 against 10.6, e2m1 6.5 against
+// 8.8).  MXFP8 activations come here with long K only.
+mx::GemvShape gemv_epi_shape(int act, int64_t N, int64_t S, int64_t M) {
+    mx::GemvShape g = dense_shape(act == ACT_MXFP8 && S < 32 ? 32 : S);
+    if (N / 16 * ((M + 15) / 16) <= 256) g.tiles = 1;
     return g;
 }
 
@@ -606,7 +616,8 @@ static mx_status linear_run(int elem, int layout, int64_t N, int64_t K, const vo
     a.y = static_cast<uint16_t *>(y);
     a.ldy = ldy;
     a.fin = fin;
-    const mx::GemvShape sh = gemv_shape(Kp / 128, false);
+    const mx::GemvShape sh =
+        fin.on ? gemv_epi_shape(act, N, Kp / 128, M) : gemv_shape(Kp / 128, false);
     log_dispatch("linear: gemv_kernel %s %s%s, %s activations, %d waves x %d-step chunks x %d "
                  "tiles; M=%lld N=%lld K=%lld",
                  elem_name(elem), layout_name(layout), with, act == ACT_BF16 ? "bf16" : "row-major MXFP8",

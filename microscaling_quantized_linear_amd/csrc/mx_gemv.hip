@@ -681,8 +681,7 @@ static hipError_t launch_g(const GemvArgs &a, const GemvShape &sh, hipStream_t s
 hipError_t launch_gemv(int elem, int layout, int act, bool moe, const GemvArgs &a,
                        const GemvShape &sh, hipStream_t st) {
     if (a.fin.on)
-        return moe ? hipErrorInvalidValue
-                   : launch_gemv_epi(elem, layout, act, a, (a.K + 127) / 128, st);
+        return moe ? hipErrorInvalidValue : launch_gemv_epi(elem, layout, act, a, sh, st);
 #define MX_GEMV_CASE(EL, LA, AC, MO)                                                     \
     if (elem == EL && layout == LA && act == AC && moe == MO)                              \
         return launch_g<EL, LA, AC, MO>(a, sh, st);
@@ -707,50 +706,41 @@ hipError_t launch_moe_combine(int64_t T, int64_t topk, int64_t N, const float *y
 
 #else  // MX_WITH_EPILOGUE
 
+// the shapes of gemv_epi_shape (mx_api.cpp)
 template <int ELEM, int LAYOUT, int ACT>
-static hipError_t launch_steps(const GemvArgs &a, int64_t steps, hipStream_t st) {
+static hipError_t launch_shape(const GemvArgs &a, const GemvShape &sh, hipStream_t st) {
     const int64_t T = a.N / 16;
-    const unsigned batches = (unsigned)((a.rows + 15) / 16);
-    const dim3 one((unsigned)T, batches), two((unsigned)((T + 1) / 2), batches);
-    // (MXFP8 activations come here with more than 64 steps only)
-    if (ACT == ACT_MXFP8 || steps >= 32) {
-        // one tile a workgroup while every tile has a compute unit of its own (N 4096, K
-        // 7168: e4m3 11.2 -> 8.8 us, e2m1 8.5 -> 7.4); else two, which share the
-        // activations (N 7168, K 4096: 8.6 against 10.6, e2m1 6.5 against 8.8)
-        if (T * batches <= 256)
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 1, true>), one, dim3(512),
-                               0, st, a);
-        else
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 8, 4, 2, true>), two, dim3(512),
-                               0, st, a);
-    } else if constexpr (ACT != ACT_MXFP8) {
-        if (steps >= 16)
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 4, 4, 1, true>), one, dim3(256), 0,
-                               st, a);
-        else if (steps >= 8)
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 2, 8, 1, true>), one, dim3(128), 0,
-                               st, a);
-        else if (steps >= 2)
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 2, 2, 1, true>), one, dim3(128), 0,
-                               st, a);
-        else
-            hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, 1, 2, 1, true>), one, dim3(64), 0,
-                               st, a);
+    const dim3 grid((unsigned)((T + sh.tiles - 1) / sh.tiles), (unsigned)((a.rows + 15) / 16));
+    const dim3 block((unsigned)(sh.nw * 64));
+#define MX_GEMV_SHAPE(NW, P, G)                                                            \
+    if (sh.nw == NW && sh.chunk == P && sh.tiles == G) {                                     \
+        hipLaunchKernelGGL((gemv_kernel<ELEM, LAYOUT, ACT, false, NW, P, G, true>), grid, block, \
+                           0, st, a);                                                      \
+        return hipGetLastError();                                                          \
     }
-    return hipGetLastError();
+    MX_GEMV_SHAPE(8, 4, 1)
+    MX_GEMV_SHAPE(8, 4, 2)
+    if constexpr (ACT != ACT_MXFP8) {
+        MX_GEMV_SHAPE(4, 4, 1)
+        MX_GEMV_SHAPE(2, 8, 1)
+        MX_GEMV_SHAPE(2, 2, 1)
+        MX_GEMV_SHAPE(1, 2, 1)
+    }
+#undef MX_GEMV_SHAPE
+    return hipErrorInvalidValue;
 }
 
-hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, int64_t steps,
+hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, const GemvShape &sh,
                            hipStream_t st) {
     if (elem == E2M1 && layout == ROW32 && act == ACT_BF16)
-        return launch_steps<E2M1, ROW32, ACT_BF16>(a, steps, st);
+        return launch_shape<E2M1, ROW32, ACT_BF16>(a, sh, st);
     if (elem != E4M3) return hipErrorInvalidValue;
     if (act == ACT_MXFP8)
-        return layout == ROW32 ? launch_steps<E4M3, ROW32, ACT_MXFP8>(a, steps, st)
-                               : launch_steps<E4M3, BLK32, ACT_MXFP8>(a, steps, st);
+        return layout == ROW32 ? launch_shape<E4M3, ROW32, ACT_MXFP8>(a, sh, st)
+                               : launch_shape<E4M3, BLK32, ACT_MXFP8>(a, sh, st);
     if (act == ACT_BF16)
-        return layout == ROW32 ? launch_steps<E4M3, ROW32, ACT_BF16>(a, steps, st)
-                               : launch_steps<E4M3, BLK32, ACT_BF16>(a, steps, st);
+        return layout == ROW32 ? launch_shape<E4M3, ROW32, ACT_BF16>(a, sh, st)
+                               : launch_shape<E4M3, BLK32, ACT_BF16>(a, sh, st);
     return hipErrorInvalidValue;
 }
 

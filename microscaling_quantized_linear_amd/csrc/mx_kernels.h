@@ -121,8 +121,8 @@ hipError_t launch_moe_combine(int64_t T, int64_t topk, int64_t N, const float *y
 hipError_t launch_gemm(int layout, const GemmArgs &a, hipStream_t stream);
 // the launchers above and those of the W8A8 GEMV hand calls with an epilogue
 // (fin.on) to these, whose kernels hold one
-hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a, int64_t steps,
-                           hipStream_t stream);
+hipError_t launch_gemv_epi(int elem, int layout, int act, const GemvArgs &a,
+                           const GemvShape &shape, hipStream_t stream);
 hipError_t launch_gemm_epi(int layout, const GemmArgs &a, hipStream_t stream);
 int gemm_tile_n(int64_t N);
 int gemm_epi_tile_n(int64_t M, int64_t N);   // with an epilogue (mx_plan.cpp)
