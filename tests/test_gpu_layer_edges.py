@@ -1,14 +1,14 @@
 """Edges of the operators between a layer's products that need cases of their own:
 gates and weights that are not finite, sums infinite or far out in an activation's
-tails."""
+tails, and the forms of the products that only larger sizes reach."""
 import numpy as np
 import pytest
 
 import layer_ref as ref
 import ops_ref
 import oracle
-from test_gpu_layer import (BF16, MXFP8, NAN16, Lin, block_inputs, check_block, g,  # noqa: F401
-                            mx, rng, run_block)
+from test_gpu_layer import (BF16, MXFP8, NAN16, T16, Lin, bf16, block_inputs, check_block,  # noqa: F401
+                            g, mx, rng, run_block)
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,51 @@ def test_linear_epilogue_tails(g, mx, elem, layout, M, N, K, act, form):
         err = np.abs(y - want)
         bad = err > of_f + 2.0 ** -8 * (np.abs(want) + of_f)
         assert not bad.any(), (kind, z[bad.any(0)][:8], y[bad][:8])
+
+
+# Sizes that reach a kernel's larger forms: layout, M, N, K, act, form, the kernel and the
+# end of its plan in the dispatch trace (tests/test_layer_trace_cpu.py holds them to it).
+LARGER = [
+    # K that the wavefronts do not share evenly, four tiles a workgroup
+    (0, 64, 4096, 96, MXFP8, "x", "gemv_w8_kernel", "1 waves x 1 steps x 4 tiles"),
+    (0, 64, 4160, 160, MXFP8, "x", "gemv_w8_kernel", "2 waves x 1 steps x 4 tiles"),
+    (1, 17, 7200, 608, MXFP8, "given", "gemv_w8_kernel", "5 waves x 1 steps x 4 tiles"),
+    (0, 64, 4096, 1568, MXFP8, "x", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
+    (1, 50, 4128, 1568, MXFP8, "given", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
+    (0, 49, 4144, 1536, T16, "t16", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
+    (1, 16, 14336, 1536, MXFP8, "given", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
+    # even K up to 4096, four tiles a workgroup
+    (0, 64, 4096, 1024, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 1 steps x 4 tiles"),
+    (1, 40, 6144, 2048, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 2 steps x 4 tiles"),
+    (1, 64, 4096, 4096, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 4 steps x 4 tiles"),
+    (0, 50, 4096, 4096, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 4 steps x 4 tiles"),
+    (1, 64, 4096, 2048, T16, "t16", "gemv_w8_even_kernel", "8 waves x 2 steps x 4 tiles"),
+    (0, 61, 4096, 4096, T16, "t16", "gemv_w8_even_kernel", "8 waves x 4 steps x 4 tiles"),
+    (0, 50, 4096, 1024, MXFP8, "given", "gemv_w8_rm_kernel", "8 waves x 1 steps x 4 tiles"),
+    # prefill, whole steps of K: tiles of 128, 224 and 256 weight rows, eight steps an
+    # iteration and a remainder
+    (0, 1025, 3600, 1024, T16, "t16", "gemm_w8a8_kernel", "128 x 256 tiles"),
+    (1, 1025, 3616, 1152, MXFP8, "x", "gemm_w8a8_kernel", "128 x 256 tiles"),
+    (0, 1800, 5376, 1024, T16, "t16", "gemm_w8a8_kernel", "224 x 256 tiles"),
+    (1, 1800, 5376, 1152, MXFP8, "x", "gemm_w8a8_kernel", "224 x 256 tiles"),
+    (1, 2500, 4064, 1024, T16, "t16", "gemm_w8a8_kernel", "256 x 256 tiles"),
+    (0, 2500, 4064, 1152, MXFP8, "given", "gemm_w8a8_kernel", "256 x 256 tiles"),
+    (1, 2500, 4064, 1152, MXFP8, "x", "gemm_w8a8_kernel", "256 x 256 tiles")]
+
+
+@pytest.mark.parametrize("layout,M,N,K,act,form,kernel,plan", LARGER)
+def test_linear_epilogue_larger_forms(g, mx, layout, M, N, K, act, form, kernel, plan):
+    r = rng(82, layout, M, N, K)
+    lin = Lin(g, r, 0, layout, M, N, K, act, rule=M % 2)
+    cases = [(ref.SILU, True, False, True), (ref.NONE, False, True, True),
+             (ref.GELU_TANH, False, True, False)]
+    if M <= 64:                          # (the definition's erfc takes its time)
+        cases.append((ref.GELU, True, True, True))
+    for n, (kind, gated, with_bias, with_res) in enumerate(cases):
+        bias = bf16(r, N) if with_bias else None
+        res = bf16(r, M, N // 2 if gated else N, scale=2) if with_res else None
+        y = lin.run(mx, form, bias, kind, gated, res, pad=8 * n)
+        out, tol = ref.epilogue(lin.z, lin.dz, bias, kind, gated, res)
+        ops_ref.assert_within(y, out, tol, f"fn {kind} gated {gated}")
+        if with_res:
+            assert np.array_equal(lin.run(mx, form, bias, kind, gated, res, pad=8 * n, inplace=True), y)

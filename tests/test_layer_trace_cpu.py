@@ -64,6 +64,14 @@ def test_gemv_shapes(host_lib, env):
         assert f"{nw} waves x {steps}-step chunks x {tiles} tiles; M={M} N={N} K={K}" in line, line
 
 
+def test_larger_forms(host_lib):
+    """The sizes that test the products' larger forms on the GPU reach them."""
+    from test_gpu_layer_edges import LARGER
+    lines = trace(host_lib, [(0, layout, M, N, K, act, form) for layout, M, N, K, act, form, *_ in LARGER])
+    for line, (*_, kernel, plan) in zip(lines, LARGER):
+        assert f"{kernel} " in line and f"{plan}; " in line, line
+
+
 def _calls(path, calls):
     """In the child process: each call, fn SiLU, no residual."""
     mx.LIB_PATH = path
