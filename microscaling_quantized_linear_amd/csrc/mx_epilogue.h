@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "mx_device.h"
 #include "mx_kernels.h"
@@ -80,13 +81,18 @@ __device__ inline float fn_value(float z, const FnCoef &c) {
     }
 }
 
-// the same by a function known at run time only (a uniform branch)
-__device__ inline float fn_any(int fn, float z, const FnCoef &c) {
+// the same of n values, by a function known at run time only (uniform branches)
+template <int n>
+__device__ inline void fn_any(int fn, float (&v)[n], const FnCoef &c) {
+    auto each = [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = fn_value<decltype(kind)::value>(v[i], c);
+    };
     const int kind = fn_kind(fn);
-    if (kind == KIND_SIMPLE) return fn_value<KIND_SIMPLE>(z, c);
-    if (kind == KIND_SILU) return fn_value<KIND_SILU>(z, c);
-    if (kind == KIND_TANH) return fn_value<KIND_TANH>(z, c);
-    return fn_value<KIND_ERF>(z, c);
+    if (kind == KIND_SIMPLE) each(std::integral_constant<int, KIND_SIMPLE>{});
+    else if (kind == KIND_SILU) each(std::integral_constant<int, KIND_SILU>{});
+    else if (kind == KIND_TANH) each(std::integral_constant<int, KIND_TANH>{});
+    else each(std::integral_constant<int, KIND_ERF>{});
 }
 
 // The decode kernels' epilogue: a lane holds the sums of weight rows n0 .. n0 + 3
@@ -115,16 +121,17 @@ __device__ inline void epi_store(const EpiArgs &f, const uint16_t *bias, const E
     if (bias)
         for (int i = 0; i < 4; ++i) v[i] += bf16_to_f32(e.bias[i]);
     if (f.gated) {
-        float h[2];
+        float h[2] = {v[0], v[2]};
+        fn_any(f.fn, h, c);
         for (int i = 0; i < 2; ++i) {
-            h[i] = fn_any(f.fn, v[2 * i], c) * v[2 * i + 1];
+            h[i] *= v[2 * i + 1];
             if (f.res) h[i] += i ? __uint_as_float(e.res[0] & 0xFFFF0000u) : bf16_to_f32(e.res[0]);
         }
         *reinterpret_cast<uint32_t *>(y + row * ldy + n0 / 2) = bf16_bits(h[0]) | bf16_bits(h[1]) << 16;
         return;
     }
+    fn_any(f.fn, v, c);
     for (int i = 0; i < 4; ++i) {
-        v[i] = fn_any(f.fn, v[i], c);
         const uint32_t r = e.res[i / 2];
         if (f.res) v[i] += i % 2 ? __uint_as_float(r & 0xFFFF0000u) : bf16_to_f32(r);
     }
