@@ -94,8 +94,9 @@ __device__ inline double sigmoid64(double v) {
     return v < 0.0 ? e * q : q;
 }
 
+// four workgroups a compute unit; three of 8-lane tokens, whose LDS takes 45 KB
 template <int LPT, int C, bool BF16, bool VEC, bool BIAS>
-__global__ void __launch_bounds__(64 * kRouteWaves, 4) route_kernel(RouteArgs p) {
+__global__ void __launch_bounds__(64 * kRouteWaves, LPT == 8 ? 3 : 4) route_kernel(RouteArgs p) {
     constexpr int TOK = 64 / LPT;                         // tokens of a wavefront
     constexpr int EP = 4 * LPT * C;                       // experts with room
     constexpr uint32_t kNone = 0x007FFFFFu;               // the number of -inf
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(64 * kRouteWaves, 4) route_kernel(RouteArgs p)
             for (int d = 0; d < 4; ++d) f[c][d] = which >> (4 * c + d) & 1u ? v[d] : f[c][d];
         }
     };
-    constexpr uint32_t kEvery = C == 8 ? ~0u : (1u << (4 * C % 32)) - 1u;
+    constexpr uint32_t kEvery = (1u << (4 * C)) - 1u;
+    static_assert(C <= 4, "a lane's experts are bits of a word");
     bool doubt = false;
     keys(doubt);
     if constexpr (BIAS)
