@@ -81,7 +81,10 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(GemvW8Args p) {
     const int n = (int)(s1 - s0);                       // <= SPW (host plan)
     const int64_t qa = s0 / 4;                          // first quad of the range
 
-    // what the epilogue reads, ahead of everything: it is not waited for then
+    // what the epilogue reads, ahead of everything.  Where a wavefront may finish more
+    // than one of four tiles (fewer than four wavefronts: known at run time only) el lies
+    // in scratch memory, 112 bytes a lane, and each tile's part is waited for here (M 64,
+    // N 4096, K 1536 on T16 input 5.0 us bare, 5.7 with SiLU and residual).
     EpiLane el[EPI ? G : 1];
     if constexpr (EPI) {
 #pragma unroll
@@ -444,9 +447,11 @@ __global__ void __launch_bounds__(NW * 64) gemv_w8_even_kernel(GemvW8Args p) {
 // With an epilogue the launch is often more than a workgroup for each compute unit (a
 // gate and up product's rows), and then it is the activations that cost: every
 // workgroup reads and quantizes all of them, as many bytes as its two tiles of weights.
-// Four tiles a workgroup halve that (gemv_w8_fused_epi_plan; two steps of weights in
-// flight then: 18.5 against 18.8 us at M 16, N 14336, K 7168).  Whole tiles go through
-// registers there too, which leaves room for two workgroups of two tiles a compute unit
+// Four tiles a workgroup halve that (gemv_w8_fused_epi_plan; of whole token tiles two
+// steps of weights in flight then: 18.5 against 18.8 us at M 16, N 14336, K 7168; of
+// partial ones that takes more than the 256 registers with row codes or the CEIL448 rule,
+// and one step is faster or within 2%: M 4 17.4-17.8 against 17.5-22.0 us, M 50, N 7168
+// 28.0-28.6 against 27.4-35.9).  Whole tiles go through registers there too, which leaves room for two workgroups of two tiles a compute unit
 // (M 16, N 28672, K 4096: 24.5 against 26.0 us; with one workgroup each, N 7168, 11.4
 // against 11.5).
 constexpr int fused_waves(bool epi, bool full, int tiles, int steps) {
@@ -456,7 +461,7 @@ template <int LAYOUT, int RULE, int G, int SPW, int NW, bool FULL, bool EPI>
 __global__ void __launch_bounds__(NW * 64, fused_waves(EPI, FULL, G, SPW))
 gemv_w8_fused_kernel(GemvW8Args p) {
     constexpr int XA = SPW > 4 ? 4 : SPW;              // steps of activations requested first
-    constexpr int WIN = EPI && G == 4 && SPW > 4 ? 2 : 1;   // steps of weight chunks in flight
+    constexpr int WIN = EPI && G == 4 && SPW > 4 && FULL ? 2 : 1;   // steps of weight chunks in flight
     constexpr int XROW = 272;                          // padded LDS row of one token
     __shared__ v4f red[NW][G][64];
     // whole tiles: activations straight into a ring of four 4 KB LDS slots

@@ -130,11 +130,13 @@ LARGER = [
     (1, 50, 4128, 1568, MXFP8, "given", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
     (0, 49, 4144, 1536, T16, "t16", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
     (1, 16, 14336, 1536, MXFP8, "given", "gemv_w8_kernel", "8 waves x 2 steps x 4 tiles"),
-    # even K up to 4096, four tiles a workgroup
+    # even K, four tiles a workgroup
     (0, 64, 4096, 1024, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 1 steps x 4 tiles"),
     (1, 40, 6144, 2048, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 2 steps x 4 tiles"),
     (1, 64, 4096, 4096, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 4 steps x 4 tiles"),
     (0, 50, 4096, 4096, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 4 steps x 4 tiles"),
+    (0, 50, 2112, 7168, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 7 steps x 4 tiles"),
+    (0, 49, 2112, 7168, MXFP8, "x", "gemv_w8_fused_kernel", "8 waves x 7 steps x 4 tiles"),
     (1, 64, 4096, 2048, T16, "t16", "gemv_w8_even_kernel", "8 waves x 2 steps x 4 tiles"),
     (0, 61, 4096, 4096, T16, "t16", "gemv_w8_even_kernel", "8 waves x 4 steps x 4 tiles"),
     (0, 50, 4096, 1024, MXFP8, "given", "gemv_w8_rm_kernel", "8 waves x 1 steps x 4 tiles"),
