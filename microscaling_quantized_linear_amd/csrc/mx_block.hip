@@ -22,7 +22,9 @@
 // the launch and three trips to memory, 4.7 us.  What was measured for it and left out, at
 // the first of these sizes: the norms' vectors loaded ahead with the row 77 us (more
 // registers, fewer rows in flight); two workgroups a compute unit that go over the rows
-// with the next one's loads in flight 85 us.
+// with the next one's loads in flight 85 us.  Rows of more than 32768 values keep 16
+// segments a wavefront: with an fp32 stream that spills 88 to 96 bytes a lane (512 rows of
+// 65536, 436 MB 109 us, 4.0 TB/s; 32768 47 us, 4.6; bf16 61 and 31).
 #include "mx_device.h"
 #include "mx_kernels.h"
 #include "mx_lanes.h"
@@ -30,8 +32,9 @@
 namespace mx {
 
 constexpr int kBlockWaves = 8;             // wavefronts of a workgroup
-// x and the residual together, up to which they are loaded through the caches: a chain
-// of such calls stays in the 256 MB of Infinity Cache (5001 rows of 1568, 31 and 47 MB:
+// x and the residual together, up to which they are loaded through the caches (the figure
+// lies between two that were measured, 55.7 and 58.7 MB): a chain of such calls stays in
+// the 256 MB of Infinity Cache (5001 rows of 1568, 31 and 47 MB:
 // 13.0 against 15.0 us, fp32 stream 18.7 against 21.9; 3400 of 4096, 56 MB: 20.4 against
 // 23.1).  Larger ones go past them (4096 rows of 7168, 117 MB: 49.2 against 54.4 us; 2048
 // rows, 59 MB: 28.7 against 29.7).

@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(256, 1) gemm_w8a8_kernel(GemmArgs p) {
         // asked for first, into the registers that the products no longer need (M and K
         // 4096, N 7168, with its quantization: 123.3 us; a slab ahead: 124.7).  No
         // product runs beside this, so an instruction for every value is 0.4 us a
-        // workgroup: a call without an activation has its own form (120.9 us).  Gated:
+        // workgroup: a call without an activation has its own form (120.9 us).  Of the forms
+        // one spills, 256 weight rows with a remainder of steps and no K tail (40 bytes a
+        // lane).  Gated:
         // rows 2 i and 2 i + 1 give column i, so dword 2 a + g of a slab's eight holds
         // columns 4 a + 2 g, + 1.
         const FnCoef fc = fn_coef(p.fin.fn);

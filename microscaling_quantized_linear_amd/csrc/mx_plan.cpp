@@ -27,7 +27,8 @@ int gemm_epi_tile_n(int64_t M, int64_t N) {
 }
 
 // The plan of the GEMV that quantizes inside, with an epilogue: four tiles a workgroup
-// instead of two, for seven steps a wavefront, where that takes fewer rounds of 256
+// instead of two, for seven steps a wavefront (K 7168 alone: the steps divide evenly),
+// where that takes fewer rounds of 256
 // workgroups by more than a third, a round of four tiles being about half as long again.
 // Measured, us at four / two (K 7168): one round against two, M 16, N 9216 15.2 / 19.2,
 // N 14336 18.5 / 20.8, N 16384 20.4 / 21.6, M 32, N 7168 14.6 / 19.9; two against four,

@@ -29,10 +29,16 @@
 // below, whose end waits for the few wavefronts that this happens to).  The result is
 // the exact choice either way.  A list that overflows (many equal numbers)
 // gives way to rounds of one expert each.
-// Bound: the wavefronts' chains of dependent steps, all tokens in one round of the
-// chip's wavefronts.  E 256, T 16384, top 8 of 4 of 8 groups: 13.2-14.0 us by box (18 MB,
-// 3.8 us of a copy's time); with 64-bit scores for all and a maximum a round 22.3.  A
-// decode step's 16 tokens: 4.0 us, launch and two trips to memory.
+// Bound: the vector instructions, all tokens in one round of the chip's wavefronts.  E
+// 256, T 16384, top 8 of 4 of 8 groups: 13.2-14.0 us by box (18 MB, 3.8 us of a copy's
+// time); 1170 vector instructions a wavefront, four wavefronts a SIMD, which issues them
+// for 19,300 of the 22,900 cycles that a wavefront lives; four times the tokens take 37
+// us.  With 64-bit scores for all and a maximum a round 22.3.  A decode step's 16 tokens:
+// 4.0 us, with a bias and groups 5.1: launch and two trips to memory.
+// More than 256 experts take the bound one by one, 32 or 64 lanes a token: E 384, top 8,
+// T 4096 / 16384 5.4 / 12.8 us (with a bias 6.2 / 15.7), E 512, top 10 5.8 / 14.3.  A list
+// that cannot hold topk + 1 and what is near them gives way to the rounds: topk 64 always,
+// 63 nearly so (E 256, T 4096 31 and 25 us, with a bias 36 and 35; topk 32 9.6 and 10.8).
 // Groups of 4, 8, .. 64 experts are scored in registers, over the lanes that hold them
 // (E 64, T 16384, 8 groups: 8.0 us, the other form 8.4), others from LDS, a lane a group, starting at its own place
 // in the group so that the lanes meet different banks.  Wavefronts are independent; LDS serves one
